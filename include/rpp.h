@@ -65,6 +65,9 @@ typedef enum rpp_dtype { RPP_F32 = 0, RPP_F16 = 1, RPP_BF16 = 2, RPP_I8 = 3 } rp
 #define RPP_DERR_TIMEOUT 2  /* a bounded wait inside a kernel gave up (pipeline stall) */
 #define RPP_DERR_ROWS 3     /* cu_seqlens[B] larger than the packed capacity T_max */
 #define RPP_DERR_TMEM 4     /* the CTAs of a paired GEMM got different tensor-memory columns */
+#define RPP_DERR_SLOT 5     /* a cache slot out of range, given twice, or not empty where it must be */
+#define RPP_DERR_PAGE 6     /* a page number outside the pool, or a page not the sequence's own */
+#define RPP_DERR_FULL 7     /* fewer free pages than a reservation needs */
 
 typedef void* rpp_stream; /* cudaStream_t */
 
@@ -448,6 +451,107 @@ RPP_API size_t rpp_patch_merge_workspace_bytes(const rpp_merge_cfg* cfg, int B);
 RPP_API rpp_status rpp_patch_merge_forward(const rpp_merge_cfg* cfg, const void* prepared, int B, const void* x,
                                            void* y, void* workspace, size_t workspace_bytes, int32_t* err,
                                            rpp_stream stream);
+
+/* ------------------------------------------------------------------------------
+ * Decoder serving: a paged key-value cache and the attention that fills and reads it.
+ * No counterpart on the pages, which stop at the encoder; the same packed rows, device
+ * lengths and error word as above.
+ *
+ * A cache is four device arrays of the caller:
+ *   pool   [layers, pages, 2, kv_heads, page_size, head_dim] of dtype, 16-byte aligned; index 0
+ *          of the third axis holds K rows, 1 V rows.  Needs no initial contents.
+ *   table  int32[slots, max_pages]: the page numbers of each sequence in order
+ *   lens   int32[slots]: tokens of the sequence in each slot; 0 = empty.  Zero at the start.
+ *   refs   int32[pages], 16-byte aligned: sequences that use the page; 0 = free.  Zero at the start.
+ * A slot uses the first ceil(lens / page_size) entries of its table row; the others are
+ * never read.  Free pages are taken lowest number first, in the order of the call's list:
+ * the state after a call depends on the state before it and nothing else.
+ *
+ * Lists of slots are device int32[n], n <= 4096.  `err` is required by the calls that change
+ * a cache.  A slot out of range, or given twice to reserve, append, fork (destinations) or free,
+ * records RPP_DERR_SLOT and changes nothing.  reserve and fork change nothing on any error;
+ * the others skip the sequence (or row) whose length or page is wrong, record
+ * RPP_DERR_LENGTH or RPP_DERR_PAGE, and stay in bounds.
+ * Calls on one cache are ordered by their stream; a cache is not to be changed on one
+ * stream while another reads it.
+ * ------------------------------------------------------------------------------ */
+typedef struct rpp_kv_cfg {
+  int layers;
+  int pages;      /* pages of the pool (in each layer) */
+  int page_size;  /* tokens a page; rpp_attention_decode needs a multiple of 16 */
+  int kv_heads;   /* kv_heads * head_dim <= 65536 */
+  int head_dim;   /* multiple of 8; rpp_attention_decode takes 64 and 128 */
+  int slots;      /* sequences; <= 65536, slots * max_pages < 2^31 */
+  int max_pages;  /* pages of one sequence at most */
+  int dtype;      /* RPP_F16 or RPP_BF16 */
+} rpp_kv_cfg;
+
+typedef struct rpp_kv_cache { /* device pointers */
+  void* pool;
+  int32_t *table, *lens, *refs;
+} rpp_kv_cache;
+
+/* Bytes of the pool; 0 for a configuration that is not valid or not supported. */
+RPP_API size_t rpp_kv_pool_bytes(const rpp_kv_cfg* cfg);
+
+/* Room for counts[i] more tokens in slot slots[i], i < n: lens grows by counts[i] and
+ * the pages that lacks are taken (refs 1).  A new sequence is a reservation in an empty
+ * slot.  RPP_DERR_LENGTH: a negative count, or a sequence longer than max_pages pages;
+ * RPP_DERR_FULL: not enough free pages. */
+RPP_API rpp_status rpp_kv_reserve(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, const int32_t* slots,
+                                  const int32_t* counts, int n, int32_t* err, rpp_stream stream);
+
+/* Writes the K and V rows of the last tokens of n sequences into one layer.
+ *  k, v        device rows of kv_heads * head_dim, row_stride elements apart (a multiple of 8,
+ *              so both may be columns of a QKV projection's output); rows_max rows
+ *  cu_seqlens  device int32[n+1]: rows cu[i] .. cu[i+1]-1 are the last tokens of slot
+ *              slots[i], in order; NULL: one row each (rows_max >= n).  Rows from cu[n] on
+ *              are not read.
+ * The rows go to positions lens - count .. lens - 1, reserved before (once for all layers).
+ * RPP_DERR_LENGTH: more rows than the sequence has tokens; RPP_DERR_PAGE: a page that is
+ * shared with another sequence; RPP_DERR_ROWS: cu[n] > rows_max. */
+RPP_API rpp_status rpp_kv_append(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* k,
+                                 const void* v, int row_stride, const int32_t* slots, const int32_t* cu_seqlens, int n,
+                                 int rows_max, int32_t* err, rpp_stream stream);
+
+/* Makes slot to[i] a copy of slot from[i], i < n: whole pages are shared (refs + 1); the
+ * rows of a last page that is not full are copied, in all layers, to a page of its own, so
+ * either sequence can grow.  from may name a slot several times.  RPP_DERR_SLOT: a
+ * destination that is not empty, or that is also a source; RPP_DERR_FULL. */
+RPP_API rpp_status rpp_kv_fork(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, const int32_t* from,
+                               const int32_t* to, int n, int32_t* err, rpp_stream stream);
+
+/* Empties n slots: refs - 1 on their pages, lens 0, table entries -1.  Pool contents stay. */
+RPP_API rpp_status rpp_kv_free(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, const int32_t* slots, int n,
+                               int32_t* err, rpp_stream stream);
+
+/* Moves the pages in use to the front of the pool: with `live` of them, the k-th page in
+ * use numbered live or above moves, in all layers, to the k-th free page below it.
+ *  table_out  device int32[slots, max_pages], refs_out int32[pages]: the cache's table and
+ *             counts afterwards (they may be the cache's own arrays; if they are not, the
+ *             old ones still describe the old places, whose rows stay until taken again)
+ *  remap      device int32[pages] out: each page's new number, -1 for a free one
+ *  live       device int32[1] out: pages in use
+ *  workspace  device, 8-byte aligned, >= rpp_kv_compact_workspace_bytes(cfg) bytes */
+RPP_API size_t rpp_kv_compact_workspace_bytes(const rpp_kv_cfg* cfg);
+RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int32_t* table_out,
+                                  int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
+                                  size_t workspace_bytes, int32_t* err, rpp_stream stream);
+
+/* Attention of one new token per sequence over the cache:
+ *   out[i, h] = sum_j softmax_j(scale * q[i, h] . K[j]) V[j],  j < lens[slots[i]],
+ * K and V of kv head h / (nh / kv_heads).  The new token's own K and V are in the cache
+ * (reserve, append) before the call; a sequence of length 0 gives zeros.
+ *  q      device rows of nh * head_dim of dtype, q_stride elements apart (a multiple of 8)
+ *  slots  device int32[n], NULL: slots 0 .. n-1; a slot may be named several times
+ *  out    device [n, nh * head_dim] of dtype
+ *  workspace  device, 256-byte aligned, >= rpp_attention_decode_workspace_bytes(cfg, n, nh)
+ *             bytes, needs no initial contents; not shared by calls that may overlap
+ * head_dim 64 or 128, page_size % 16 == 0 (RPP_EUNSUPPORTED otherwise), nh % kv_heads == 0. */
+RPP_API size_t rpp_attention_decode_workspace_bytes(const rpp_kv_cfg* cfg, int n, int nh);
+RPP_API rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* q,
+                                        int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,
+                                        void* workspace, size_t workspace_bytes, int32_t* err, rpp_stream stream);
 
 #ifdef __cplusplus
 }

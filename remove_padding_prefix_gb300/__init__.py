@@ -17,8 +17,9 @@ import torch
 
 from . import _abi
 from ._abi import (RPP_F32, RPP_F16, RPP_BF16, RPP_I8, RPP_EPI_BIAS, RPP_EPI_BIAS_GELU,  # noqa: F401
-                   RPP_EPI_BIAS_RESIDUAL, RPP_DERR_LENGTH, RPP_DERR_TIMEOUT, RPP_DERR_ROWS, RPP_DERR_TMEM, EncoderCfg, LayerSrc,
-                   SwinCfg, SwinSrc, MergeCfg)
+                   RPP_EPI_BIAS_RESIDUAL, RPP_DERR_LENGTH, RPP_DERR_TIMEOUT, RPP_DERR_ROWS, RPP_DERR_TMEM,
+                   RPP_DERR_SLOT, RPP_DERR_PAGE, RPP_DERR_FULL, EncoderCfg, LayerSrc, SwinCfg, SwinSrc, MergeCfg, KvCfg,
+                   KvArrays)
 
 __all__ = [
     "RppError", "lib", "torch_dtype", "dtype_code", "build_offsets", "remove_padding", "rebuild_padding", "linear",
@@ -26,6 +27,8 @@ __all__ = [
     "encoder_layer_calibrate", "encoder_forward", "quantize_weight", "quantize_activation", "gemm_i8_i32",
     "swin_cfg", "SwinBlock", "swin_prepare_bias", "window_attention_forward", "swin_block_forward",
     "merge_cfg", "PatchMerge", "patch_merge_forward",
+    "KvCache", "kv_reserve", "kv_append", "kv_fork", "kv_free", "kv_compact",
+    "attention_decode_workspace", "attention_decode",
     "get_device_error", "new_error_word",
 ]
 
@@ -364,3 +367,173 @@ def patch_merge_forward(pm: PatchMerge, x, B: int, y=None, workspace=None, err=N
            lib().rpp_patch_merge_forward(C.byref(pm.cfg), _p(pm.block), B, _p(x), _p(out), _p(ws), ws.numel(),
                                          _p(err), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- decoder serving: paged key-value cache
+def _on(dev, *tensors):
+    """Every tensor on the device of the cache, which is the current one (a launch goes there)."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, not on the current device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"expected a tensor on {dev}, got one on {t.device}")
+
+
+def _ints(name, t, n=None):
+    if t.dtype is not torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name}: expected a contiguous int32 tensor" + (f" of {n}" if n is not None else ""))
+
+
+def _rows(name, t, width, dtype):
+    """A 2D view of 16-bit rows whose columns are contiguous; returns the row stride in elements."""
+    if t.dim() != 2 or t.shape[1] != width or t.dtype is not dtype or t.stride(1) != 1:
+        raise ValueError(f"{name}: expected rows of {width} contiguous {dtype}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+class KvCache:
+    """A paged key-value cache: the pool [layers, pages, 2, kv_heads, page_size, head_dim] and
+    its table, lens and refs (include/rpp.h, "Decoder serving"), in device memory.
+
+    ``err`` is the device error word that the calls use when none is given."""
+
+    def __init__(self, layers, pages, page_size, kv_heads, head_dim, slots, max_pages, dtype="bf16", device="cuda"):
+        self._bind(torch.empty(layers, pages, 2, kv_heads, page_size, head_dim, dtype=torch_dtype(dtype),
+                               device=device),
+                   torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(slots, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device))
+        self.err = new_error_word(self.device)
+
+    @classmethod
+    def from_tensors(cls, pool, table, lens, refs):
+        """A cache over arrays that the caller holds already (kept, not copied)."""
+        c = cls.__new__(cls)
+        c._bind(pool, table, lens, refs)
+        c.err = new_error_word(c.device)
+        return c
+
+    def _bind(self, pool, table, lens, refs):
+        if pool.dim() != 6 or pool.shape[2] != 2 or not pool.is_contiguous():
+            raise ValueError("pool: expected a contiguous [layers, pages, 2, kv_heads, page_size, head_dim] tensor")
+        if table.dim() != 2:
+            raise ValueError("table: expected [slots, max_pages]")
+        _ints("table", table)
+        _ints("lens", lens, table.shape[0])
+        _ints("refs", refs, pool.shape[1])
+        if not all(t.is_cuda and t.device == pool.device for t in (pool, table, lens, refs)):
+            raise ValueError("expected CUDA tensors on one device")
+        self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
+        layers, pages, _, heads, rows, d = pool.shape
+        self.cfg = KvCfg(layers, pages, rows, heads, d, table.shape[0], table.shape[1], dtype_code(pool.dtype))
+        self.device = pool.device
+        if lib().rpp_kv_pool_bytes(C.byref(self.cfg)) == 0:
+            raise RppError("rpp_kv_pool_bytes", _abi.RPP_EUNSUPPORTED)
+        self._arrays = KvArrays(pool.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
+        self._cfg, self._cache = C.byref(self.cfg), C.byref(self._arrays)
+
+    def adopt(self, table, refs):
+        """Take the table and counts that kv_compact wrote to arrays of their own."""
+        self._bind(self.pool, table, self.lens, refs)
+
+    def _err(self, err):
+        return self.err.data_ptr() if err is None else _p(err)
+
+
+def kv_reserve(cache: KvCache, slots, counts, err=None, stream=None):
+    """Room for counts[i] more tokens in slot slots[i] (both device int32[n])."""
+    n = slots.numel()
+    _on(cache.device, slots, counts, err)
+    _ints("slots", slots)
+    _ints("counts", counts, n)
+    _check("rpp_kv_reserve", lib().rpp_kv_reserve(cache._cfg, cache._cache, _p(slots), _p(counts), n,
+                                                  cache._err(err), _stream(stream)))
+
+
+def kv_append(cache: KvCache, layer: int, k, v, slots, cu_seqlens=None, err=None, stream=None):
+    """Write the K and V rows of the last tokens of each sequence into one layer.
+
+    k, v: [rows, kv_heads * head_dim] (column ranges of one QKV projection's output will
+    do); rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 belong to slots[i], or row i without
+    cu_seqlens."""
+    n, width = slots.numel(), cache.cfg.kv_heads * cache.cfg.head_dim
+    _on(cache.device, k, v, slots, cu_seqlens, err)
+    _ints("slots", slots)
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, n + 1)
+    ld = _rows("k", k, width, cache.pool.dtype)
+    if _rows("v", v, width, cache.pool.dtype) != ld or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v: expected equal row counts and strides")
+    _check("rpp_kv_append", lib().rpp_kv_append(cache._cfg, cache._cache, layer, _p(k), _p(v), ld, _p(slots),
+                                                _p(cu_seqlens), n, k.shape[0], cache._err(err), _stream(stream)))
+
+
+def kv_fork(cache: KvCache, src, dst, err=None, stream=None):
+    """Slot dst[i] (empty) becomes a copy of slot src[i]; whole pages are shared."""
+    n = src.numel()
+    _on(cache.device, src, dst, err)
+    _ints("src", src)
+    _ints("dst", dst, n)
+    _check("rpp_kv_fork", lib().rpp_kv_fork(cache._cfg, cache._cache, _p(src), _p(dst), n, cache._err(err),
+                                            _stream(stream)))
+
+
+def kv_free(cache: KvCache, slots, err=None, stream=None):
+    """Empty the slots; pages that no sequence uses any more become free."""
+    _on(cache.device, slots, err)
+    _ints("slots", slots)
+    _check("rpp_kv_free", lib().rpp_kv_free(cache._cfg, cache._cache, _p(slots), slots.numel(), cache._err(err),
+                                            _stream(stream)))
+
+
+def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, workspace=None, err=None, stream=None):
+    """Move the pages in use to the front of the pool; returns (table, refs, live).
+
+    Without table_out and refs_out the cache's own arrays are rewritten; with them the old
+    ones stay as they are (KvCache.adopt takes the new).  live: device int32[1]."""
+    dev, cfg = cache.device, cache.cfg
+    table = cache.table if table_out is None else table_out
+    refs = cache.refs if refs_out is None else refs_out
+    _on(dev, table, refs, remap, workspace, err)
+    _ints("table_out", table, cache.table.numel())
+    _ints("refs_out", refs, cfg.pages)
+    if remap is None:
+        remap = torch.empty(cfg.pages, dtype=torch.int32, device=dev)
+    _ints("remap", remap, cfg.pages)
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(lib().rpp_kv_compact_workspace_bytes(cache._cfg), dtype=torch.uint8, device=dev)
+    _check("rpp_kv_compact", lib().rpp_kv_compact(cache._cfg, cache._cache, _p(table), _p(refs), _p(remap), _p(live),
+                                                  _p(workspace), workspace.numel(), cache._err(err),
+                                                  _stream(stream)))
+    return table, refs, live
+
+
+def attention_decode_workspace(cache: KvCache, n: int, nh: int) -> torch.Tensor:
+    nbytes = lib().rpp_attention_decode_workspace_bytes(cache._cfg, n, nh)
+    if nbytes == 0:
+        raise RppError("rpp_attention_decode_workspace_bytes", _abi.RPP_EINVAL)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+
+
+def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=None, workspace=None, err=None,
+                     stream=None):
+    """Attention of one new token per sequence over the cache.
+
+    q: [n, nh * head_dim] (a column range of a QKV projection's output will do); slots:
+    device int32[n], or None for slots 0 .. n - 1; scale: 1 / sqrt(head_dim) by default."""
+    d = cache.cfg.head_dim
+    n, nh = q.shape[0], q.shape[1] // d
+    _on(cache.device, q, slots, out, workspace, err)
+    if slots is not None:
+        _ints("slots", slots, n)
+    ld = _rows("q", q, nh * d, cache.pool.dtype)
+    o = out if out is not None else torch.empty(n, nh * d, dtype=q.dtype, device=q.device)
+    if o.shape != (n, nh * d) or o.dtype is not q.dtype or not o.is_contiguous():
+        raise ValueError("out: expected a contiguous tensor like q")
+    ws = workspace if workspace is not None else attention_decode_workspace(cache, n, nh)
+    _check("rpp_attention_decode",
+           lib().rpp_attention_decode(cache._cfg, cache._cache, layer, _p(q), ld, _p(slots), n, nh,
+                                      d ** -0.5 if scale is None else scale, _p(o), _p(ws), ws.numel(),
+                                      cache._err(err), _stream(stream)))
+    return o

@@ -14,6 +14,7 @@ RPP_OK, RPP_EINVAL, RPP_EUNSUPPORTED, RPP_ECUDA, RPP_EWORKSPACE, RPP_EDEVICE = 0
 RPP_F32, RPP_F16, RPP_BF16, RPP_I8 = 0, 1, 2, 3
 RPP_EPI_BIAS, RPP_EPI_BIAS_GELU, RPP_EPI_BIAS_RESIDUAL = 0, 1, 2
 RPP_DERR_LENGTH, RPP_DERR_TIMEOUT, RPP_DERR_ROWS, RPP_DERR_TMEM = 1, 2, 3, 4
+RPP_DERR_SLOT, RPP_DERR_PAGE, RPP_DERR_FULL = 5, 6, 7
 
 vp = C.c_void_p
 i32 = C.c_int
@@ -38,6 +39,15 @@ class SwinCfg(C.Structure):
 
 class MergeCfg(C.Structure):
     _fields_ = [("img", i32), ("channels", i32), ("eps", f32), ("dtype", i32)]
+
+
+class KvCfg(C.Structure):
+    _fields_ = [(n, i32) for n in ("layers", "pages", "page_size", "kv_heads", "head_dim", "slots", "max_pages",
+                                   "dtype")]
+
+
+class KvArrays(C.Structure):
+    _fields_ = [(n, vp) for n in ("pool", "table", "lens", "refs")]
 
 
 class SwinSrc(C.Structure):
@@ -86,6 +96,16 @@ SIGNATURES = {
     "rpp_patch_merge_prepare": (i32, [C.POINTER(MergeCfg), vp, vp, vp, vp, vp]),
     "rpp_patch_merge_workspace_bytes": (sz, [C.POINTER(MergeCfg), i32]),
     "rpp_patch_merge_forward": (i32, [C.POINTER(MergeCfg), vp, i32, vp, vp, vp, sz, vp, vp]),
+    "rpp_kv_pool_bytes": (sz, [C.POINTER(KvCfg)]),
+    "rpp_kv_reserve": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, vp, i32, vp, vp]),
+    "rpp_kv_append": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), i32, vp, vp, i32, vp, vp, i32, i32, vp, vp]),
+    "rpp_kv_fork": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, vp, i32, vp, vp]),
+    "rpp_kv_free": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, i32, vp, vp]),
+    "rpp_kv_compact_workspace_bytes": (sz, [C.POINTER(KvCfg)]),
+    "rpp_kv_compact": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, vp, vp, vp, vp, sz, vp, vp]),
+    "rpp_attention_decode_workspace_bytes": (sz, [C.POINTER(KvCfg), i32, i32]),
+    "rpp_attention_decode": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), i32, vp, i32, vp, i32, i32, f32, vp, vp, sz,
+                                   vp, vp]),
 }
 
 _lib = None

@@ -156,6 +156,37 @@ cudaError_t launch_patch_merge_ln(const void* x, int B, int I, int C, rpp_dtype 
 cudaError_t launch_attention_varlen(const void* qkv, const int32_t* cu, int B, int T_max, int max_len, int nh, int d,
                                     rpp_dtype dtype, void* out, int32_t* err, cudaStream_t stream);
 
+// paged key-value cache (kv_cache.cu): sizes, and the device arrays of one cache
+struct KvDims {
+  int layers, pages, page_size, kv_heads, head_dim, slots, max_pages;
+};
+struct KvState {
+  void* pool;        // [layers, pages, 2, kv_heads, page_size, head_dim], 16-bit
+  int32_t* table;    // [slots, max_pages]
+  int32_t* lens;     // [slots]
+  int32_t* refs;     // [pages]
+};
+constexpr int kKvMaxList = 4096;      // entries of a slot list (held in shared memory)
+constexpr int kKvMaxSlots = 65536;    // slots of a cache (a bitmap of them is held in shared memory)
+cudaError_t launch_kv_reserve(const KvDims& d, const KvState& c, const int32_t* slots, const int32_t* counts, int n,
+                              int32_t* err, cudaStream_t stream);
+cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* from, const int32_t* to, int n,
+                           int32_t* err, cudaStream_t stream);
+cudaError_t launch_kv_free(const KvDims& d, const KvState& c, const int32_t* slots, int n, int32_t* err,
+                           cudaStream_t stream);
+cudaError_t launch_kv_append(const KvDims& d, const KvState& c, int layer, const void* k, const void* v,
+                             int row_stride, const int32_t* slots, const int32_t* cu, int n, int rows_max,
+                             int32_t* err, cudaStream_t stream);
+// moves: int32[2 + 2 * (pages / 2)] scratch, 8-byte aligned
+cudaError_t launch_kv_compact(const KvDims& d, const KvState& c, int32_t* table_out, int32_t* refs_out, int32_t* remap,
+                              int32_t* live, int32_t* moves, int32_t* err, cudaStream_t stream);
+
+// single-token attention over a paged cache (attention_decode.cu); ws: attention_decode_ws_bytes
+size_t attention_decode_ws_bytes(int n, int nh, int nkv, int d);
+cudaError_t launch_attention_decode(const KvDims& d, const KvState& c, rpp_dtype dtype, int layer, const void* q,
+                                    int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,
+                                    void* ws, int32_t* err, cudaStream_t stream);
+
 bool window_attention_supported(int C, int nh, int w, int I, int s);
 cudaError_t launch_window_attention(int B, const void* qkv, const float* bias, void* out, int C, int nh, int I, int w,
                                     int s, rpp_dtype dtype, int32_t* err, cudaStream_t stream);
