@@ -538,6 +538,22 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
                                   int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
                                   size_t workspace_bytes, int32_t* err, rpp_stream stream);
 
+/* Causal attention over packed prompts of different lengths, grouped heads: for row i of
+ * sequence b (rows cu[b] .. cu[b+1]-1) and head h
+ *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j]) v[j],  cu[b] <= j <= i,
+ * k and v of kv head h / (nh / nkv).  Rows that a query must not see have no effect on
+ * it, whatever they hold (infinities and NaN among it).
+ *  q       device rows of nh * d of dtype, q_stride elements apart; k, v: rows of nkv * d,
+ *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
+ *          QKV projection's output); T_max rows each
+ *  out     device [T_max, nh * d] of dtype; rows >= cu[B] untouched; may alias none of q, k, v
+ * d 64 or 128; dtype RPP_F16 or RPP_BF16; nh % nkv == 0; B <= 4096; every length <= max_len <=
+ * 262144 (RPP_DERR_LENGTH; RPP_DERR_ROWS if cu[B] > T_max). */
+RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, const void* v, int q_stride,
+                                               int kv_stride, const int32_t* cu_seqlens, int B, int T_max,
+                                               int max_len, int nh, int nkv, int d, rpp_dtype dtype, float scale,
+                                               void* out, int32_t* err, rpp_stream stream);
+
 /* Attention of one new token per sequence over the cache:
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . K[j]) V[j],  j < lens[slots[i]],
  * K and V of kv head h / (nh / kv_heads).  The new token's own K and V are in the cache

@@ -28,7 +28,7 @@ __all__ = [
     "swin_cfg", "SwinBlock", "swin_prepare_bias", "window_attention_forward", "swin_block_forward",
     "merge_cfg", "PatchMerge", "patch_merge_forward",
     "KvCache", "kv_reserve", "kv_append", "kv_fork", "kv_free", "kv_compact",
-    "attention_decode_workspace", "attention_decode",
+    "attention_causal_varlen", "attention_decode_workspace", "attention_decode",
     "get_device_error", "new_error_word",
 ]
 
@@ -507,6 +507,26 @@ def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, worksp
                                                   _p(workspace), workspace.numel(), cache._err(err),
                                                   _stream(stream)))
     return table, refs, live
+
+
+def attention_causal_varlen(q, k, v, cu_seqlens, B: int, max_len: int, nh: int, nkv: int, d: int, scale=None, out=None,
+                            err=None, stream=None):
+    """Causal attention over packed prompts: q [T_max, nh * d], k and v [T_max, nkv * d] (column
+    ranges of one QKV projection's output will do), scale 1 / sqrt(d) by default."""
+    T_max = q.shape[0]
+    _on(q.device, k, v, cu_seqlens, out, err)
+    _ints("cu_seqlens", cu_seqlens, B + 1)
+    ldq, ld = _rows("q", q, nh * d, q.dtype), _rows("k", k, nkv * d, q.dtype)
+    if _rows("v", v, nkv * d, q.dtype) != ld or k.shape[0] != T_max or v.shape[0] != T_max:
+        raise ValueError("q, k and v: expected equal row counts, k and v equal strides")
+    o = out if out is not None else torch.empty(T_max, nh * d, dtype=q.dtype, device=q.device)
+    if o.shape != (T_max, nh * d) or o.dtype is not q.dtype or not o.is_contiguous():
+        raise ValueError("out: expected a contiguous tensor like q")
+    _check("rpp_attention_causal_varlen",
+           lib().rpp_attention_causal_varlen(_p(q), _p(k), _p(v), ldq, ld, _p(cu_seqlens), B, T_max, max_len, nh, nkv,
+                                             d, dtype_code(q.dtype), d ** -0.5 if scale is None else scale, _p(o),
+                                             _p(err), _stream(stream)))
+    return o
 
 
 def attention_decode_workspace(cache: KvCache, n: int, nh: int) -> torch.Tensor:

@@ -103,6 +103,8 @@ SIGNATURES = {
     "rpp_kv_free": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, i32, vp, vp]),
     "rpp_kv_compact_workspace_bytes": (sz, [C.POINTER(KvCfg)]),
     "rpp_kv_compact": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, vp, vp, vp, vp, sz, vp, vp]),
+    "rpp_attention_causal_varlen": (i32, [vp, vp, vp, i32, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp,
+                                          vp]),
     "rpp_attention_decode_workspace_bytes": (sz, [C.POINTER(KvCfg), i32, i32]),
     "rpp_attention_decode": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), i32, vp, i32, vp, i32, i32, f32, vp, vp, sz,
                                    vp, vp]),

@@ -137,3 +137,23 @@ rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache
                                                   q, q_stride, slots, n, nh, scale, out, workspace, err,
                                                   static_cast<cudaStream_t>(stream)));
 }
+
+rpp_status rpp_attention_causal_varlen(const void* q, const void* k, const void* v, int q_stride, int kv_stride,
+                                       const int32_t* cu_seqlens, int B, int T_max, int max_len, int nh, int nkv,
+                                       int d, rpp_dtype dtype, float scale, void* out, int32_t* err,
+                                       rpp_stream stream) {
+  if (!q || !k || !v || !cu_seqlens || !out || B <= 0 || T_max <= 0 || max_len <= 0 || nh <= 0 || nkv <= 0 ||
+      nh % nkv || d <= 0)
+    return RPP_EINVAL;
+  if (!(scale > 0.f) || scale > 3.0e38f) return RPP_EINVAL;
+  if (dtype != RPP_F16 && dtype != RPP_BF16) return RPP_EUNSUPPORTED;
+  if (!attention_causal_supported(B, max_len, d)) return RPP_EUNSUPPORTED;
+  if ((static_cast<long long>(T_max) / 128 + B) * nh > 0x7fffffffLL ||
+      static_cast<long long>(nh) * d > 0x7fffffffLL)
+    return RPP_EUNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || q_stride % 8 || kv_stride % 8 ||
+      q_stride < nh * d || kv_stride < nkv * d)
+    return RPP_EINVAL;
+  const CausalArgs a{q, k, v, q_stride, kv_stride, cu_seqlens, B, T_max, max_len, nh, nkv, d, dtype, scale, out, err};
+  return status_from_cuda(launch_attention_causal(a, static_cast<cudaStream_t>(stream)));
+}

@@ -129,9 +129,10 @@ void set_gemm_stall_next(unsigned long long limit_ns);
 cudaError_t launch_gemm_f32(const float* a, const float* w_t, const float* bias, const float* residual, float* out,
                             int M_max, const int32_t* rows, int N, int K, int epi, int32_t* err, cudaStream_t stream);
 
-// 2D row-major [rows, cols] tensor map, box = box_cols x box_rows (defined with the GEMM)
+// 2D row-major [rows, cols] tensor map, box = box_cols x box_rows, rows row_stride elements
+// apart (0: cols) (defined with the GEMM)
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, long long rows,
-                  int cols, int box_rows, int box_cols, CUtensorMapSwizzle swz);
+                  int cols, int box_rows, int box_cols, CUtensorMapSwizzle swz, int row_stride = 0);
 // persistent longest-first tcgen05 varlen attention (S, P, O in tensor memory), head size 64
 bool attention_sched_supported(int B, int max_len);
 // i8_scales: device (s_q, s_k, s_v) for int8 codes held in bf16 (dtype RPP_BF16, fp16 out);
@@ -186,6 +187,20 @@ size_t attention_decode_ws_bytes(int n, int nh, int nkv, int d);
 cudaError_t launch_attention_decode(const KvDims& d, const KvState& c, rpp_dtype dtype, int layer, const void* q,
                                     int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,
                                     void* ws, int32_t* err, cudaStream_t stream);
+
+// causal attention over packed prompts (attention_causal.cu); strides in elements
+struct CausalArgs {
+  const void *q, *k, *v;   // rows of nh * d, nkv * d, nkv * d
+  int q_stride, kv_stride;
+  const int32_t* cu;       // [B + 1]
+  int B, T_max, max_len, nh, nkv, d;
+  rpp_dtype dtype;
+  float scale;
+  void* out;               // [T_max, nh * d]
+  int32_t* err;
+};
+bool attention_causal_supported(int B, int max_len, int d);
+cudaError_t launch_attention_causal(const CausalArgs& a, cudaStream_t stream);
 
 bool window_attention_supported(int C, int nh, int w, int I, int s);
 cudaError_t launch_window_attention(int B, const void* qkv, const float* bias, void* out, int C, int nh, int I, int w,

@@ -117,3 +117,22 @@ def test_sizes(lib):
     assert 0 < small < lib.rpp_attention_decode_workspace_bytes(C.byref(c), 1, 32)
     assert lib.rpp_attention_decode_workspace_bytes(C.byref(c), 1, 3) == 0      # not a multiple of the kv heads
     assert lib.rpp_attention_decode_workspace_bytes(C.byref(c), 4097, 2) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), EINVAL), (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(cu=None), EINVAL),
+    (dict(out=None), EINVAL), (dict(B=0), EINVAL), (dict(T=0), EINVAL), (dict(max_len=0), EINVAL), (dict(nh=0), EINVAL),
+    (dict(nkv=0), EINVAL), (dict(nh=5), EINVAL), (dict(d=0), EINVAL), (dict(q=264), EINVAL), (dict(v=258), EINVAL),
+    (dict(out=8), EINVAL), (dict(ldq=260), EINVAL), (dict(ldq=248), EINVAL), (dict(ld=127), EINVAL), (dict(ld=120), EINVAL),
+    (dict(scale=0.0), EINVAL), (dict(scale=float("nan")), EINVAL),
+    (dict(dtype=_abi.RPP_F32), EUNSUPPORTED), (dict(dtype=_abi.RPP_I8), EUNSUPPORTED),
+    (dict(d=96, ldq=1024, ld=1024), EUNSUPPORTED), (dict(B=4097), EUNSUPPORTED), (dict(max_len=262145), EUNSUPPORTED),
+    (dict(nh=1 << 24, T=1 << 20, ldq=1 << 30), EUNSUPPORTED),
+])
+def test_causal_arguments(lib, kw, status):
+    g = dict(q=256, k=256, v=256, ldq=256, ld=128, cu=256, B=3, T=100, max_len=60, nh=4, nkv=2, d=64,
+             dtype=_abi.RPP_BF16, scale=0.125, out=256)
+    g.update(kw)
+    assert lib.rpp_attention_causal_varlen(g["q"], g["k"], g["v"], g["ldq"], g["ld"], g["cu"], g["B"], g["T"],
+                                           g["max_len"], g["nh"], g["nkv"], g["d"], g["dtype"], g["scale"], g["out"],
+                                           None, None) == status

@@ -1,0 +1,224 @@
+"""Causal attention over packed prompts, against fp64.
+
+Tolerance, per output element, from the arithmetic (e = eps of the 16-bit type, so a rounding is off by
+e / 2 of the value):
+  * the final rounding: e / 2 |o|;
+  * the weights are rounded to the type before the product with V: e / 2 of sum_j w_j |v_j|, w the
+    softmax (their sum is taken before the rounding); fp16 weights below 2^-14 are off by up to 2^-25, n of
+    them, against a sum of at least 1: n 2^-25 max |v|;
+  * a score is an fp32 sum of d exact products, off by at most (d + 2) 2^-24 sum |q_c k_c|, and a base change
+    off by 2^-23 of it, in the exponent; exp2 off by 2^-22; fp32 sums over n keys by n 2^-24: each times
+    max |v|, twice (numerator and sum).
+"""
+import numpy as np
+import pytest
+import torch
+
+import remove_padding_prefix_gb300 as rpp
+from gpu_util import TDT, dev
+
+pytestmark = pytest.mark.gpu
+
+EPS = {torch.float16: 2.0 ** -10, torch.bfloat16: 2.0 ** -7}
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=dev())
+
+
+def cu_of(lens):
+    return [0] + [int(x) for x in np.cumsum(lens)]
+
+
+def make(lens, nh, nkv, d, dtype, seed=0, spare=0, pad=0, qscale=2.0):
+    """q, k, v as columns of one QKV tensor (pad columns before them); rows behind the last sequence hold NaN."""
+    T = sum(lens)
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    x = torch.randn((T + spare, pad + (nh + 2 * nkv) * d), generator=g, device=dev())
+    x[:, pad:pad + nh * d] *= qscale
+    x = x.to(TDT[dtype])
+    x[T:] = float("nan")
+    a, b = pad + nh * d, pad + (nh + nkv) * d
+    return x[:, pad:a], x[:, a:b], x[:, b:b + nkv * d]
+
+
+def check_rows(got, q, k, v, cu, nh, nkv, d, scale=None, seqs=None, heads=None):
+    scale = d ** -0.5 if scale is None else scale
+    e = EPS[q.dtype]
+    for b in seqs if seqs is not None else range(len(cu) - 1):
+        a, z = cu[b], cu[b + 1]
+        n = z - a
+        if n == 0:
+            continue
+        hide = torch.ones((n, n), dtype=torch.bool, device=dev()).triu(1)
+        for h in heads if heads is not None else range(nh):
+            c, kc = slice(h * d, (h + 1) * d), slice(h // (nh // nkv) * d, (h // (nh // nkv) + 1) * d)
+            Q, K, V = q[a:z, c].double(), k[a:z, kc].double(), v[a:z, kc].double()
+            s = (Q @ K.T * scale).masked_fill(hide, float("-inf"))
+            w = torch.softmax(s, 1)
+            ref = w @ V
+            mag = (Q.abs() @ K.abs().T * scale).masked_fill(hide, 0).amax(1, keepdim=True)
+            big = s.masked_fill(hide, 0).abs().amax(1, keepdim=True)
+            vmax = V.abs().max()
+            ds = (d + 2) * 2.0 ** -24 * mag + 2.0 ** -23 * big
+            limit = e / 2 * ref.abs() + e / 2 * (1 + e) * (w @ V.abs()) + vmax * (
+                2 * ds + 2 * (2.0 ** -22 + n * 2.0 ** -24) + n * 2.0 ** -25) + 2.0 ** -25
+            o = got[a:z, c].double()
+            assert torch.isfinite(o).all(), (b, h, n)
+            off = (o - ref).abs()
+            assert (off <= limit).all(), (b, h, n, float((off / limit).max()))
+
+
+def run(lens, nh, nkv, d, dtype, seed=0, spare=0, pad=0, max_len=None, scale=None, **kw):
+    q, k, v = make(lens, nh, nkv, d, dtype, seed, spare, pad)
+    cu = cu_of(lens)
+    err = rpp.new_error_word()
+    out = torch.full((q.shape[0], nh * d), 7.0, dtype=q.dtype, device=dev())
+    rpp.attention_causal_varlen(q, k, v, ints(cu), len(lens), max_len or max(lens), nh, nkv, d, scale=scale, out=out,
+                                err=err)
+    assert rpp.get_device_error(err) == 0
+    check_rows(out, q, k, v, cu, nh, nkv, d, scale, **kw)
+    assert (out[cu[-1]:] == 7).all()          # rows behind the last sequence stay as they were
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 17, 127, 128])
+def test_one_tile(dtype, d, n):
+    run([n], 2, 2, d, dtype, seed=n, spare=3)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [129, 255, 256, 257, 383, 384, 385, 511, 513, 640, 1000, 1025])
+def test_tiles(dtype, d, n):
+    run([n], 3, 1, d, dtype, seed=n, spare=1)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh,nkv", [(1, 1), (8, 2), (12, 12), (5, 1), (6, 3), (32, 8)])
+def test_ragged_batches(dtype, d, nh, nkv):
+    run([1, 0, 300, 128, 5, 129, 0, 256, 77, 257, 640, 2, 0], nh, nkv, d, dtype, seed=nh, spare=50, pad=8)
+
+
+@pytest.mark.parametrize("d,max_len", [(64, 128), (128, 128), (64, 100), (128, 2000), (64, 262144)])
+def test_max_len_above_the_lengths(d, max_len):
+    run([100, 3, 0, 50, 1], 4, 2, d, "bf16", max_len=max_len)
+
+
+@pytest.mark.parametrize("B,hi", [(300, 12), (4096, 5), (700, 150), (64, 384)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_prompts(B, hi, d):
+    lens = [int(x) for x in np.random.default_rng(B).integers(0, hi + 1, B)]
+    run(lens, 2, 1, d, "bf16", seqs=list(range(0, B, max(1, B // 150))) + [B - 1])
+
+
+@pytest.mark.parametrize("dtype,d,nh,nkv,lens", [("bf16", 128, 8, 2, [5000, 1, 3001]), ("fp16", 64, 4, 4, [6007]),
+                                                 ("bf16", 64, 16, 1, [2500, 2500, 40])])
+def test_long(dtype, d, nh, nkv, lens):
+    run(lens, nh, nkv, d, dtype, heads=[0, nh - 1])
+
+
+def test_scale_and_rows_apart():
+    run([300, 40], 4, 2, 64, "fp16", scale=0.4, pad=24)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[600, 90], [128], [100]])
+def test_scores_far_apart(d, lens):
+    """Scores that climb along the keys, by far more than the lazily moved maximum allows."""
+    q, k, v = make(lens, 2, 1, d, "fp16")
+    T = sum(lens)
+    k.zero_()
+    k[:, 0] = torch.linspace(-200, 200, T, device=dev()).half()
+    q.zero_()
+    q[:, ::d] = 4.0
+    err = rpp.new_error_word()
+    out = rpp.attention_causal_varlen(q, k, v, ints(cu_of(lens)), len(lens), max(lens), 2, 1, d, err=err)
+    assert rpp.get_device_error(err) == 0
+    check_rows(out, q, k, v, cu_of(lens), 2, 1, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,where", [([300, 200], [5, 127, 128, 130, 255, 256, 299]), ([100, 28], [0, 50, 99]),
+                                        ([513], [256, 383, 384, 511, 512])])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_what_a_row_must_not_see_stays_out(d, lens, where, what):
+    """NaN and infinities in one key or value row: rows before it, and other sequences, as without it; rows
+    from it on as the formula has them."""
+    q, k, v = make(lens, 2, 1, d, "bf16")
+    cu = cu_of(lens)
+    base = rpp.attention_causal_varlen(q, k, v, ints(cu), len(lens), max(lens), 2, 1, d)
+    for j in where:
+        for bad in (float("nan"), float("inf"), float("-inf")):
+            k2, v2 = k.clone(), v.clone()
+            (k2 if what == "k" else v2)[j, 3] = bad
+            err = rpp.new_error_word()
+            out = rpp.attention_causal_varlen(q, k2, v2, ints(cu), len(lens), max(lens), 2, 1, d, err=err)
+            assert rpp.get_device_error(err) == 0
+            assert torch.equal(out[:j], base[:j])
+            assert torch.equal(out[lens[0]:], base[lens[0]:])
+            if what == "v":
+                seen = out[j:lens[0]].float()
+                for h in range(2):
+                    col = seen[:, h * d + 3]
+                    assert (torch.isnan(col) if bad != bad else col == bad).all()
+                    keep = torch.ones(2 * d, dtype=torch.bool, device=dev())
+                    keep[[3, d + 3]] = False
+                    assert torch.isfinite(seen[:, keep]).all()
+
+
+def test_the_same_result_every_time():
+    lens = [int(x) for x in np.random.default_rng(1).integers(1, 900, 40)]
+    q, k, v = make(lens, 8, 2, 128, "bf16")
+    a = (q, k, v, ints(cu_of(lens)), len(lens), 900, 8, 2, 128)
+    first = rpp.attention_causal_varlen(*a)
+    for _ in range(5):
+        assert torch.equal(first, rpp.attention_causal_varlen(*a))
+
+
+def test_device_errors():
+    q, k, v = make([100, 28], 2, 1, 64, "bf16")
+    for cu, max_len, code in (([0, 100, 129], 128, rpp.RPP_DERR_ROWS), ([0, 100, 128], 99, rpp.RPP_DERR_LENGTH),
+                              ([0, 100, 50], 128, rpp.RPP_DERR_ROWS), ([-4, 100, 128], 128, rpp.RPP_DERR_ROWS)):
+        err = rpp.new_error_word()
+        out = torch.full((128, 128), 7.0, dtype=torch.bfloat16, device=dev())
+        rpp.attention_causal_varlen(q, k, v, ints(cu), 2, max_len, 2, 1, 64, out=out, err=err)
+        assert rpp.get_device_error(err) == code
+        assert (out == 7).all()
+    err.fill_(42)
+    rpp.attention_causal_varlen(q, k, v, ints([0, 100, 128]), 2, 128, 2, 1, 64, out=out, err=err)
+    assert (out == 7).all() and rpp.get_device_error(err) == 42
+
+
+def test_after_other_tensor_memory_users():
+    """Tensor memory keeps what the kernel before left (NaN here): it must not reach an output."""
+    q, k, v = make([700, 3], 2, 1, 128, "bf16")
+    bad = torch.full_like(q, float("nan"))
+    for _ in range(3):
+        rpp.attention_causal_varlen(bad, k, v, ints([0, 700, 703]), 2, 700, 2, 1, 128)
+        run([130, 1, 300], 4, 2, 128, "bf16")
+        run([130, 1, 300], 4, 2, 64, "bf16")
+
+
+def test_captured_and_replayed_with_other_lengths():
+    nh, nkv, d, T = 4, 2, 64, 1200
+    q, k, v = make([T], nh, nkv, d, "bf16")
+    cu = ints([0, T, T, T])
+    err = rpp.new_error_word()
+    out = torch.empty(T, nh * d, dtype=torch.bfloat16, device=dev())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            rpp.attention_causal_varlen(q, k, v, cu, 3, T, nh, nkv, d, out=out, err=err)
+    torch.cuda.synchronize()
+    for lens in ([1200, 0, 0], [0, 0, 0], [1, 600, 599], [128, 128, 128], [5, 0, 1000]):
+        cu.copy_(ints(cu_of(lens)))
+        out.fill_(7)
+        g.replay()
+        assert rpp.get_device_error(err) == 0
+        check_rows(out, q, k, v, cu_of(lens), nh, nkv, d)
+        assert (out[sum(lens):] == 7).all()
