@@ -47,12 +47,14 @@ def lib():
     return _abi.load()
 
 
+_CODE = {t: code for code, t in _TORCH.items()}
+
+
 def dtype_code(dt) -> int:
     if isinstance(dt, str):
         return _DT[dt]
-    for code, t in _TORCH.items():
-        if t == dt:
-            return code
+    if dt in _CODE:
+        return _CODE[dt]
     raise ValueError(dt)
 
 
@@ -370,25 +372,30 @@ def patch_merge_forward(pm: PatchMerge, x, B: int, y=None, workspace=None, err=N
 
 
 # ---------------------------------------------------------------- decoder serving: paged key-value cache
-def _on(dev, *tensors):
-    """Every tensor on the device of the cache, which is the current one (a launch goes there)."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, not on the current device")
+# These calls take a few microseconds on the GPU at their smallest, so their checks use the cheap
+# accessors: get_device() (-1 off the GPU, so it also says whether there is one) and one
+# reading each of shape and stride.
+def _here(*tensors) -> int:
+    """The current device's raw stream, once every tensor given is on that device."""
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"expected a tensor on {dev}, got one on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected a tensor on the current device (cuda:{dev}), got one on {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _ints(name, t, n=None):
     if t.dtype is not torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{name}: expected a contiguous int32 tensor" + (f" of {n}" if n is not None else ""))
+    return t.data_ptr()
 
 
-def _rows(name, t, width, dtype):
+def _rows(name, t, width, dtype) -> int:
     """A 2D view of 16-bit rows whose columns are contiguous; returns the row stride in elements."""
-    if t.dim() != 2 or t.shape[1] != width or t.dtype is not dtype or t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width or stride[1] != 1 or t.dtype is not dtype:
         raise ValueError(f"{name}: expected rows of {width} contiguous {dtype}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    return stride[0] if shape[0] > 1 else max(stride[0], width)
 
 
 class KvCache:
@@ -403,15 +410,22 @@ class KvCache:
                    torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(slots, dtype=torch.int32, device=device),
                    torch.zeros(pages, dtype=torch.int32, device=device))
-        self.err = new_error_word(self.device)
+        self._own()
 
     @classmethod
     def from_tensors(cls, pool, table, lens, refs):
         """A cache over arrays that the caller holds already (kept, not copied)."""
         c = cls.__new__(cls)
         c._bind(pool, table, lens, refs)
-        c.err = new_error_word(c.device)
+        c._own()
         return c
+
+    def _own(self):
+        self.err = new_error_word(self.pool.device)
+        nbytes = lib().rpp_kv_compact_workspace_bytes(self._cfg)
+        # kv_compact's lists: of the cache, as the calls that change one are ordered anyway
+        self._remap = torch.empty(self.cfg.pages, dtype=torch.int32, device=self.pool.device)
+        self._lists = torch.empty(nbytes, dtype=torch.uint8, device=self.pool.device)
 
     def _bind(self, pool, table, lens, refs):
         if pool.dim() != 6 or pool.shape[2] != 2 or not pool.is_contiguous():
@@ -426,28 +440,26 @@ class KvCache:
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         layers, pages, _, heads, rows, d = pool.shape
         self.cfg = KvCfg(layers, pages, rows, heads, d, table.shape[0], table.shape[1], dtype_code(pool.dtype))
-        self.device = pool.device
-        if lib().rpp_kv_pool_bytes(C.byref(self.cfg)) == 0:
+        self._cfg = C.byref(self.cfg)
+        if lib().rpp_kv_pool_bytes(self._cfg) == 0:
             raise RppError("rpp_kv_pool_bytes", _abi.RPP_EUNSUPPORTED)
         self._arrays = KvArrays(pool.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
-        self._cfg, self._cache = C.byref(self.cfg), C.byref(self._arrays)
+        self._cache = C.byref(self._arrays)
+        self._dtype, self._d, self._width = pool.dtype, d, heads * d
 
     def adopt(self, table, refs):
         """Take the table and counts that kv_compact wrote to arrays of their own."""
         self._bind(self.pool, table, self.lens, refs)
 
-    def _err(self, err):
-        return self.err.data_ptr() if err is None else _p(err)
-
 
 def kv_reserve(cache: KvCache, slots, counts, err=None, stream=None):
     """Room for counts[i] more tokens in slot slots[i] (both device int32[n])."""
+    err = cache.err if err is None else err
+    here = _here(cache.pool, slots, counts, err)
     n = slots.numel()
-    _on(cache.device, slots, counts, err)
-    _ints("slots", slots)
-    _ints("counts", counts, n)
-    _check("rpp_kv_reserve", lib().rpp_kv_reserve(cache._cfg, cache._cache, _p(slots), _p(counts), n,
-                                                  cache._err(err), _stream(stream)))
+    _check("rpp_kv_reserve", lib().rpp_kv_reserve(cache._cfg, cache._cache, _ints("slots", slots),
+                                                  _ints("counts", counts, n), n, err.data_ptr(),
+                                                  here if stream is None else stream.cuda_stream))
 
 
 def kv_append(cache: KvCache, layer: int, k, v, slots, cu_seqlens=None, err=None, stream=None):
@@ -456,76 +468,81 @@ def kv_append(cache: KvCache, layer: int, k, v, slots, cu_seqlens=None, err=None
     k, v: [rows, kv_heads * head_dim] (column ranges of one QKV projection's output will
     do); rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 belong to slots[i], or row i without
     cu_seqlens."""
-    n, width = slots.numel(), cache.cfg.kv_heads * cache.cfg.head_dim
-    _on(cache.device, k, v, slots, cu_seqlens, err)
-    _ints("slots", slots)
-    if cu_seqlens is not None:
-        _ints("cu_seqlens", cu_seqlens, n + 1)
-    ld = _rows("k", k, width, cache.pool.dtype)
-    if _rows("v", v, width, cache.pool.dtype) != ld or k.shape[0] != v.shape[0]:
+    err = cache.err if err is None else err
+    here = _here(cache.pool, k, v, slots, cu_seqlens, err)
+    n, rows = slots.numel(), k.shape[0]
+    ld = _rows("k", k, cache._width, cache._dtype)
+    if _rows("v", v, cache._width, cache._dtype) != ld or v.shape[0] != rows:
         raise ValueError("k and v: expected equal row counts and strides")
-    _check("rpp_kv_append", lib().rpp_kv_append(cache._cfg, cache._cache, layer, _p(k), _p(v), ld, _p(slots),
-                                                _p(cu_seqlens), n, k.shape[0], cache._err(err), _stream(stream)))
+    _check("rpp_kv_append",
+           lib().rpp_kv_append(cache._cfg, cache._cache, layer, k.data_ptr(), v.data_ptr(), ld, _ints("slots", slots),
+                               None if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, n + 1), n, rows,
+                               err.data_ptr(), here if stream is None else stream.cuda_stream))
 
 
 def kv_fork(cache: KvCache, src, dst, err=None, stream=None):
     """Slot dst[i] (empty) becomes a copy of slot src[i]; whole pages are shared."""
+    err = cache.err if err is None else err
+    here = _here(cache.pool, src, dst, err)
     n = src.numel()
-    _on(cache.device, src, dst, err)
-    _ints("src", src)
-    _ints("dst", dst, n)
-    _check("rpp_kv_fork", lib().rpp_kv_fork(cache._cfg, cache._cache, _p(src), _p(dst), n, cache._err(err),
-                                            _stream(stream)))
+    _check("rpp_kv_fork", lib().rpp_kv_fork(cache._cfg, cache._cache, _ints("src", src), _ints("dst", dst, n), n,
+                                            err.data_ptr(), here if stream is None else stream.cuda_stream))
 
 
 def kv_free(cache: KvCache, slots, err=None, stream=None):
     """Empty the slots; pages that no sequence uses any more become free."""
-    _on(cache.device, slots, err)
-    _ints("slots", slots)
-    _check("rpp_kv_free", lib().rpp_kv_free(cache._cfg, cache._cache, _p(slots), slots.numel(), cache._err(err),
-                                            _stream(stream)))
+    err = cache.err if err is None else err
+    here = _here(cache.pool, slots, err)
+    _check("rpp_kv_free", lib().rpp_kv_free(cache._cfg, cache._cache, _ints("slots", slots), slots.numel(),
+                                            err.data_ptr(), here if stream is None else stream.cuda_stream))
 
 
-def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, workspace=None, err=None, stream=None):
+def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, live=None, err=None, stream=None):
     """Move the pages in use to the front of the pool; returns (table, refs, live).
 
     Without table_out and refs_out the cache's own arrays are rewritten; with them the old
-    ones stay as they are (KvCache.adopt takes the new).  live: device int32[1]."""
-    dev, cfg = cache.device, cache.cfg
+    ones stay as they are (KvCache.adopt takes the new).  live: device int32[1]; remap:
+    device int32[pages], each page's new number, for tables of the caller's own."""
+    err = cache.err if err is None else err
     table = cache.table if table_out is None else table_out
     refs = cache.refs if refs_out is None else refs_out
-    _on(dev, table, refs, remap, workspace, err)
-    _ints("table_out", table, cache.table.numel())
-    _ints("refs_out", refs, cfg.pages)
-    if remap is None:
-        remap = torch.empty(cfg.pages, dtype=torch.int32, device=dev)
-    _ints("remap", remap, cfg.pages)
-    live = torch.empty(1, dtype=torch.int32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(lib().rpp_kv_compact_workspace_bytes(cache._cfg), dtype=torch.uint8, device=dev)
-    _check("rpp_kv_compact", lib().rpp_kv_compact(cache._cfg, cache._cache, _p(table), _p(refs), _p(remap), _p(live),
-                                                  _p(workspace), workspace.numel(), cache._err(err),
-                                                  _stream(stream)))
+    remap = cache._remap if remap is None else remap
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=cache.pool.device)
+    here = _here(cache.pool, table, refs, remap, live, err)
+    cfg, lists = cache.cfg, cache._lists
+    _check("rpp_kv_compact",
+           lib().rpp_kv_compact(cache._cfg, cache._cache, _ints("table_out", table, cfg.slots * cfg.max_pages),
+                                _ints("refs_out", refs, cfg.pages), _ints("remap", remap, cfg.pages),
+                                _ints("live", live, 1), lists.data_ptr(), lists.numel(), err.data_ptr(),
+                                here if stream is None else stream.cuda_stream))
     return table, refs, live
+
+
+def _out_like(q, out, rows, width):
+    if out is None:
+        return torch.empty((rows, width), dtype=q.dtype, device=q.device)
+    if out.shape != (rows, width) or out.dtype is not q.dtype or not out.is_contiguous():
+        raise ValueError("out: expected a contiguous tensor like q")
+    return out
 
 
 def attention_causal_varlen(q, k, v, cu_seqlens, B: int, max_len: int, nh: int, nkv: int, d: int, scale=None, out=None,
                             err=None, stream=None):
     """Causal attention over packed prompts: q [T_max, nh * d], k and v [T_max, nkv * d] (column
     ranges of one QKV projection's output will do), scale 1 / sqrt(d) by default."""
-    T_max = q.shape[0]
-    _on(q.device, k, v, cu_seqlens, out, err)
-    _ints("cu_seqlens", cu_seqlens, B + 1)
-    ldq, ld = _rows("q", q, nh * d, q.dtype), _rows("k", k, nkv * d, q.dtype)
-    if _rows("v", v, nkv * d, q.dtype) != ld or k.shape[0] != T_max or v.shape[0] != T_max:
+    here = _here(q, k, v, cu_seqlens, out, err)
+    T_max, dtype = q.shape[0], q.dtype
+    ldq, ld = _rows("q", q, nh * d, dtype), _rows("k", k, nkv * d, dtype)
+    if _rows("v", v, nkv * d, dtype) != ld or k.shape[0] != T_max or v.shape[0] != T_max:
         raise ValueError("q, k and v: expected equal row counts, k and v equal strides")
-    o = out if out is not None else torch.empty(T_max, nh * d, dtype=q.dtype, device=q.device)
-    if o.shape != (T_max, nh * d) or o.dtype is not q.dtype or not o.is_contiguous():
-        raise ValueError("out: expected a contiguous tensor like q")
+    o = _out_like(q, out, T_max, nh * d)
     _check("rpp_attention_causal_varlen",
-           lib().rpp_attention_causal_varlen(_p(q), _p(k), _p(v), ldq, ld, _p(cu_seqlens), B, T_max, max_len, nh, nkv,
-                                             d, dtype_code(q.dtype), d ** -0.5 if scale is None else scale, _p(o),
-                                             _p(err), _stream(stream)))
+           lib().rpp_attention_causal_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ld,
+                                             _ints("cu_seqlens", cu_seqlens, B + 1), B, T_max, max_len, nh, nkv, d,
+                                             dtype_code(dtype), d ** -0.5 if scale is None else scale, o.data_ptr(),
+                                             None if err is None else err.data_ptr(),
+                                             here if stream is None else stream.cuda_stream))
     return o
 
 
@@ -533,7 +550,7 @@ def attention_decode_workspace(cache: KvCache, n: int, nh: int) -> torch.Tensor:
     nbytes = lib().rpp_attention_decode_workspace_bytes(cache._cfg, n, nh)
     if nbytes == 0:
         raise RppError("rpp_attention_decode_workspace_bytes", _abi.RPP_EINVAL)
-    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.pool.device)
 
 
 def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=None, workspace=None, err=None,
@@ -542,18 +559,17 @@ def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=
 
     q: [n, nh * head_dim] (a column range of a QKV projection's output will do); slots:
     device int32[n], or None for slots 0 .. n - 1; scale: 1 / sqrt(head_dim) by default."""
-    d = cache.cfg.head_dim
-    n, nh = q.shape[0], q.shape[1] // d
-    _on(cache.device, q, slots, out, workspace, err)
-    if slots is not None:
-        _ints("slots", slots, n)
-    ld = _rows("q", q, nh * d, cache.pool.dtype)
-    o = out if out is not None else torch.empty(n, nh * d, dtype=q.dtype, device=q.device)
-    if o.shape != (n, nh * d) or o.dtype is not q.dtype or not o.is_contiguous():
-        raise ValueError("out: expected a contiguous tensor like q")
-    ws = workspace if workspace is not None else attention_decode_workspace(cache, n, nh)
+    err = cache.err if err is None else err
+    d = cache._d
+    n, width = q.shape
+    nh = width // d
+    ws = attention_decode_workspace(cache, n, nh) if workspace is None else workspace
+    here = _here(cache.pool, q, slots, out, ws, err)
+    ld = _rows("q", q, nh * d, cache._dtype)
+    o = _out_like(q, out, n, nh * d)
     _check("rpp_attention_decode",
-           lib().rpp_attention_decode(cache._cfg, cache._cache, layer, _p(q), ld, _p(slots), n, nh,
-                                      d ** -0.5 if scale is None else scale, _p(o), _p(ws), ws.numel(),
-                                      cache._err(err), _stream(stream)))
+           lib().rpp_attention_decode(cache._cfg, cache._cache, layer, q.data_ptr(), ld,
+                                      None if slots is None else _ints("slots", slots, n), n, nh,
+                                      d ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                      err.data_ptr(), here if stream is None else stream.cuda_stream))
     return o

@@ -34,6 +34,8 @@
 // with positive weights are the elements themselves).  Every mbarrier wait is bounded; a
 // wait that gives up records RPP_DERR_TIMEOUT and the CTA drains, frees tensor memory
 // and exits.
+#include <algorithm>
+
 #include "attention_common.cuh"
 
 namespace rpp {
@@ -174,7 +176,8 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
 template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(Shape<D, NQ>::kThreads, NQ == 2 ? 1 : 2)
     attention_causal_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                            const __grid_constant__ CUtensorMap tv, const T* __restrict__ v_rows, int kv_stride,
+                            const __grid_constant__ CUtensorMap tv, int q_x, int k_x, int v_x,
+                            const T* __restrict__ v_rows, int kv_stride,
                             const int32_t* __restrict__ cu, int B, int T_max, int max_len, int nh, int group,
                             int classes, T* __restrict__ out, float scale_log2, int32_t* err) {
   using S = Shape<D, NQ>;
@@ -275,17 +278,18 @@ __global__ void __launch_bounds__(Shape<D, NQ>::kThreads, NQ == 2 ? 1 : 2)
           mbar_arrive_expect_tx(&q_full[x], S::kTileBytes);
 #pragma unroll
           for (int c = 0; c < HB; ++c)
-            tma_load_2d(sQ + x * S::kTileBytes + c * kBox, &tq, &q_full[x], it.h * D + 64 * c, it.c0 + it.q0 + x * kT);
+            tma_load_2d(sQ + x * S::kTileBytes + c * kBox, &tq, &q_full[x], q_x + it.h * D + 64 * c,
+                        it.c0 + it.q0 + x * kT);
           ++nq[x];
           return true;
         };
         // Q_0 K_0 before Q_1: the first scores of query tile 0 are issued before the last ones of
         // the previous item's query tile 1, which Q_1 waits for
-        ok = load_q(0) && load(&tk, kv_col, it.c0);
+        ok = load_q(0) && load(&tk, k_x + kv_col, it.c0);
         if constexpr (NQ == 2) ok = ok && load_q(1);
-        ok = ok && load(&tv, kv_col, it.c0);
+        ok = ok && load(&tv, v_x + kv_col, it.c0);
         for (int j = 1; j < n && ok; ++j)
-          ok = load(&tk, kv_col, it.c0 + j * kT) && load(&tv, kv_col, it.c0 + j * kT);
+          ok = load(&tk, k_x + kv_col, it.c0 + j * kT) && load(&tv, v_x + kv_col, it.c0 + j * kT);
       }
       if (!ok) {
         set_device_error(err, RPP_DERR_TIMEOUT);
@@ -568,31 +572,35 @@ __global__ void __launch_bounds__(Shape<D, NQ>::kThreads, NQ == 2 ? 1 : 2)
   }
 }
 
+// The tensor maps of a call, and where the columns of q, k and v start in them.
+struct Maps {
+  CUtensorMap q, k, v;
+  int q_x = 0, k_x = 0, v_x = 0;
+};
+
 template <typename T, int D, int NQ>
-cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CausalArgs& a,
-                   cudaStream_t stream) {
+cudaError_t launch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
   using S = Shape<D, NQ>;
   constexpr int ROWS = NQ * kT;
   const int classes = (a.max_len + ROWS - 1) / ROWS;
   const size_t smem = 1024 + S::kOffList + list_bytes(a.B, classes);
-  const cudaError_t e = cudaFuncSetAttribute(attention_causal_kernel<T, D, NQ>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(1024 + S::kOffList + list_bytes(kMaxPrompts, kMaxCausalLen / ROWS)));
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(attention_causal_kernel<T, D, NQ>,
+                                    1024 + S::kOffList + list_bytes(kMaxPrompts, kMaxCausalLen / ROWS));
   if (e != cudaSuccess) return e;
   // never more CTAs than items: ceil(len / ROWS) <= len / ROWS + 1 for each sequence
   const long long most = (static_cast<long long>(a.T_max) / ROWS + a.B) * a.nh;
   const long long room = static_cast<long long>(NQ == 2 ? 1 : 2) * num_sms();
   const int grid = static_cast<int>(most < room ? most : room);
-  return launch_pdl(attention_causal_kernel<T, D, NQ>, dim3(grid), dim3(S::kThreads), smem, stream, tq, tk, tv,
-                    static_cast<const T*>(a.v), a.kv_stride, a.cu, a.B, a.T_max, a.max_len, a.nh, a.nh / a.nkv, classes,
-                    static_cast<T*>(a.out), a.scale * 1.4426950408889634f, a.err);
+  return launch_pdl(attention_causal_kernel<T, D, NQ>, dim3(grid), dim3(S::kThreads), smem, stream, t.q, t.k, t.v,
+                    t.q_x, t.k_x, t.v_x, static_cast<const T*>(a.v), a.kv_stride, a.cu, a.B, a.T_max, a.max_len, a.nh,
+                    a.nh / a.nkv, classes, static_cast<T*>(a.out), a.scale * 1.4426950408889634f, a.err);
 }
 
 template <typename T>
-cudaError_t dispatch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CausalArgs& a, int nq,
-                     cudaStream_t stream) {
-  if (a.d == 64) return nq == 2 ? launch<T, 64, 2>(tq, tk, tv, a, stream) : launch<T, 64, 1>(tq, tk, tv, a, stream);
-  return nq == 2 ? launch<T, 128, 2>(tq, tk, tv, a, stream) : launch<T, 128, 1>(tq, tk, tv, a, stream);
+cudaError_t dispatch(const Maps& t, const CausalArgs& a, int nq, cudaStream_t stream) {
+  if (a.d == 64) return nq == 2 ? launch<T, 64, 2>(t, a, stream) : launch<T, 64, 1>(t, a, stream);
+  return nq == 2 ? launch<T, 128, 2>(t, a, stream) : launch<T, 128, 1>(t, a, stream);
 }
 
 }  // namespace
@@ -604,14 +612,29 @@ bool attention_causal_supported(int B, int max_len, int d) {
 cudaError_t launch_attention_causal(const CausalArgs& a, cudaStream_t stream) {
   const CUtensorMapDataType dt =
       a.dtype == RPP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap tq, tk, tv;
-  if (!make_tmap_2d(&tq, a.q, dt, 2, a.T_max, a.nh * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.q_stride) ||
-      !make_tmap_2d(&tk, a.k, dt, 2, a.T_max, a.nkv * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.kv_stride) ||
-      !make_tmap_2d(&tv, a.v, dt, 2, a.T_max, a.nkv * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.kv_stride))
+  Maps t;
+  // Columns of one projection's output: one map over all of them (encoding one takes about as
+  // long on the host as the rest of the call before the launch).
+  const uintptr_t q = reinterpret_cast<uintptr_t>(a.q), k = reinterpret_cast<uintptr_t>(a.k),
+                  v = reinterpret_cast<uintptr_t>(a.v);
+  const uintptr_t first = std::min(q, std::min(k, v));
+  const uintptr_t end = std::max(q + 2u * static_cast<uintptr_t>(a.nh) * a.d,
+                                 std::max(k, v) + 2u * static_cast<uintptr_t>(a.nkv) * a.d);
+  if (a.q_stride == a.kv_stride && end - first <= 2u * static_cast<uintptr_t>(a.q_stride)) {
+    if (!make_tmap_2d(&t.q, reinterpret_cast<const void*>(first), dt, 2, a.T_max, static_cast<int>((end - first) / 2),
+                      kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.q_stride))
+      return cudaErrorInvalidValue;
+    t.k = t.v = t.q;
+    t.q_x = static_cast<int>((q - first) / 2);
+    t.k_x = static_cast<int>((k - first) / 2);
+    t.v_x = static_cast<int>((v - first) / 2);
+  } else if (!make_tmap_2d(&t.q, a.q, dt, 2, a.T_max, a.nh * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.q_stride) ||
+             !make_tmap_2d(&t.k, a.k, dt, 2, a.T_max, a.nkv * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.kv_stride) ||
+             !make_tmap_2d(&t.v, a.v, dt, 2, a.T_max, a.nkv * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.kv_stride)) {
     return cudaErrorInvalidValue;
+  }
   const int nq = a.max_len > kT ? 2 : 1;
-  return a.dtype == RPP_F16 ? dispatch<__half>(tq, tk, tv, a, nq, stream)
-                            : dispatch<__nv_bfloat16>(tq, tk, tv, a, nq, stream);
+  return a.dtype == RPP_F16 ? dispatch<__half>(t, a, nq, stream) : dispatch<__nv_bfloat16>(t, a, nq, stream);
 }
 
 }  // namespace rpp

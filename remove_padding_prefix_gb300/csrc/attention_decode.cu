@@ -543,8 +543,9 @@ inline int decode_ctas() { return num_sms(); }
 template <typename T, int D>
 cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
   const size_t smem = kRingBytes + (static_cast<size_t>(p.n) + 1) * sizeof(long long);
-  const cudaError_t a = cudaFuncSetAttribute(attention_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kRingBytes + (kKvMaxList + 1) * sizeof(long long)));
+  static SmemLimit limit;
+  const cudaError_t a =
+      limit.raise(attention_decode_kernel<T, D>, kRingBytes + (kKvMaxList + 1) * sizeof(long long));
   if (a != cudaSuccess) return a;
   const int ctas = decode_ctas();
   const cudaError_t e = launch_pdl(attention_decode_kernel<T, D>, dim3(ctas), dim3(kWarps * 32), smem, stream, p);

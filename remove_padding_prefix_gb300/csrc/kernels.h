@@ -1,5 +1,6 @@
 // Internal launchers shared by the kernel translation units and the C ABI (api.cu).
 #pragma once
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -7,6 +8,25 @@
 namespace rpp {
 
 int num_sms();   // SM count of the current device (cached per device)
+
+// Raises a kernel's dynamic shared memory limit on the current device, once per device (the
+// attribute is the device's, and setting it costs a part of a launch).  Two callers at once may
+// both set it, to the same value.
+struct SmemLimit {
+  std::atomic<bool> set[64] = {};
+  template <typename K>
+  cudaError_t raise(K* kernel, size_t bytes) {
+    int dev = -1;
+    const cudaError_t g = cudaGetDevice(&dev);
+    if (g != cudaSuccess) return g;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && known) set[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 // Status of the C ABI for a CUDA runtime result; clears a sticky launch error.  Shared
 // by every entry point so that the same failure maps to the same status everywhere.

@@ -222,3 +222,16 @@ def test_captured_and_replayed_with_other_lengths():
         assert rpp.get_device_error(err) == 0
         check_rows(out, q, k, v, cu_of(lens), nh, nkv, d)
         assert (out[sum(lens):] == 7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_q_k_and_v_as_tensors_of_their_own(d):
+    """Three tensors (three tensor maps), and K and V in the order V, K inside one."""
+    lens, nh, nkv = [300, 1, 130], 4, 2
+    q, k, v = make(lens, nh, nkv, d, "bf16")
+    kv = torch.cat([v, k], 1)
+    want = rpp.attention_causal_varlen(q, k, v, ints(cu_of(lens)), 3, 300, nh, nkv, d)
+    check_rows(want, q, k, v, cu_of(lens), nh, nkv, d)
+    for a in ((q.contiguous(), k.contiguous(), v.contiguous()), (q, kv[:, nkv * d:], kv[:, :nkv * d]),
+              (q.contiguous(), kv[:, nkv * d:], kv[:, :nkv * d])):
+        assert torch.equal(rpp.attention_causal_varlen(*a, ints(cu_of(lens)), 3, 300, nh, nkv, d), want)
