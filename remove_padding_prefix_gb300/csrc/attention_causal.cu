@@ -13,6 +13,7 @@
 //               d = 128: S and O fill the CTA's 256 columns, so P takes the place of S and the
 //               order is PV(j), S(j + 1).  d = 64: P has columns of its own and S(j + 1) is issued
 //               once the scores of S(j) have been read.  S(0) of the next item follows the same way.
+//   warps 2, 3  look over the V tiles that reach past the item's first query (below).
 //   warps 4-7   softmax, one thread a query row, all 128 scores of a tile in registers (the
 //               producers' warpgroup gives up registers for that): no exchange between
 //               threads.  Running maximum moved only when it grows by more than 8 (log2
@@ -27,10 +28,11 @@
 // of the costs without a counter in memory.
 //
 // What a row must not see stays out of it: scores past the row become -inf before the
-// maximum.  P is 0 there, but 0 * inf is not, so in the diagonal tile V rows past the
-// sequence are zeroed in shared memory, and elements of V that are not finite are
+// maximum.  P is 0 there, but 0 * inf is not, so in the tiles on the diagonal V rows past
+// the sequence are zeroed in shared memory, and elements of V that are not finite are
 // taken out before the product and added back to the rows that may see them (their sums
-// with positive weights are the elements themselves).  Every mbarrier wait is bounded; a
+// with positive weights are the elements themselves).  Two warps do that for every V tile
+// before the product may read it, so their wait on a ring slot is never a phase off.  Every mbarrier wait is bounded; a
 // wait that gives up records RPP_DERR_TIMEOUT and the CTA drains, frees tensor memory
 // and exits.
 #include <algorithm>
@@ -45,16 +47,19 @@ using attn::neg_inf;
 using attn::pack2;
 using attn::tc_mma_f16_tmem_a;
 
-constexpr int kT = 128;                  // queries and keys of a tile
+constexpr int kT = 128;                  // queries of an item, keys of a tile
 constexpr int kMaxPrompts = 4096;        // sequences of a call (their bounds are held in shared memory)
 constexpr int kMaxCausalLen = 262144;    // tokens of a sequence (its tile counts are held there too)
 
 template <int D>
 struct Shape {
   static constexpr uint32_t kTileBytes = kT * D * 2;
-  static constexpr bool kApart = D == 64;          // P in columns of its own
-  static constexpr int kQ = D == 64 ? 2 : 1;       // Q buffers
-  static constexpr int kSlots = D == 64 ? 4 : 2;   // ring of K / V tiles (two CTAs' shared memory in 227 KB)
+  static constexpr bool kApart = D == 64;                  // P in columns of its own
+  static constexpr int kQ = D == 64 ? 2 : 1;               // Q buffers
+  // Ring of K / V tiles (two CTAs' shared memory in 227 KB).  An even number, so that a slot is K's or
+  // V's for good: who waits for V tiles only must not find a K tile's phase in between.
+  static constexpr int kSlots = D == 64 ? 4 : 2;
+  static constexpr int kVSlots = kSlots / 2;               // V's, in turn
   static constexpr uint32_t kColP = kApart ? 192 : 0, kColO = 128;   // S at column 0
   static constexpr uint32_t kOffRing = kQ * kTileBytes;
   static constexpr uint32_t kOffStage = kOffRing + kSlots * kTileBytes;   // 2 KB a softmax warp: rows on their way out
@@ -62,35 +67,39 @@ struct Shape {
   static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
   static constexpr uint32_t kOffList = kOffMisc + 32;
 };
-constexpr int kThreads = 256;            // warps 0-3: TMA, MMA, two idle; warps 4-7: softmax
+constexpr int kThreads = 256;            // warps 0-3: TMA, MMA, V's watch; warps 4-7: softmax
 constexpr uint32_t kTmemCols = 256;
+// Registers: launched with 128 a thread, 32768 a CTA (checked at the first launch: a split above
+// what the launch has would wait for ever); 128 threads keep 64, the softmax's 128 take 192.
+constexpr int kLaunchRegs = 128, kLowRegs = 64, kHighRegs = 192;
+static_assert(128 * (kLowRegs + kHighRegs) == kLaunchRegs * kThreads, "the split must be the launch's registers");
 
-// the item list in shared memory: cu_seqlens, sequences by falling number of items, and
-// for each place i in a sequence how many items lie at later places
+// The item list: in shared memory the sequences by falling number of items and, for each place i
+// in a sequence, how many items lie at later places.
 struct List {
-  const int* cu;          // [B + 1]
+  const int32_t* cu;      // [B + 1], in global memory
   const int16_t* perm;    // [sequences with an item]
-  const int* first;       // [classes + 1]: first item at place i; first[0] + its own = all
+  const int* first;       // [classes + 1]: first item at place i; [classes]: all items
   int classes, nh, total;
   float inv_nh;
 };
+__host__ __device__ constexpr uint32_t perm_bytes(int B) { return (static_cast<uint32_t>(B) * 2u + 15u) / 16u * 16u; }
 __host__ __device__ constexpr uint32_t list_bytes(int B, int classes) {
-  return (static_cast<uint32_t>(B + 1) * 4u + 15u) / 16u * 16u + (static_cast<uint32_t>(B) * 2u + 15u) / 16u * 16u +
-         static_cast<uint32_t>(2 * classes + 3) * 4u;
+  return perm_bytes(B) + static_cast<uint32_t>(classes + 1) * 4u;
 }
 
 struct CausalItem {
   int b, h, q0, c0, len;
+  __device__ __forceinline__ int tiles() const { return q0 / kT + 1; }   // key tiles up to the diagonal
 };
 
 // A walk over the list by rising item number.  The place of an item in its sequence falls
-// along the list, so after the first search it is a step or none; where only the number of
-// key tiles (place + 1) is wanted, nothing is divided.
+// along the list, so after the first search it is a step or none.
 struct Walk {
   const List& s;
   int place;
   __device__ __forceinline__ explicit Walk(const List& l) : s(l), place(-1) {}
-  __device__ __forceinline__ int tiles(int g) {
+  __device__ __forceinline__ void seek(int g) {
     if (place < 0) {                    // the smallest place with first[place] <= g
       int lo = 0, hi = s.classes - 1;
       while (lo < hi) {
@@ -102,11 +111,15 @@ struct Walk {
     } else {
       while (place > 0 && s.first[place - 1] <= g) --place;
     }
+  }
+  __device__ __forceinline__ int tiles(int g) {   // of item g: nothing is divided
+    seek(g);
     return place + 1;
   }
   __device__ __forceinline__ CausalItem at(int g) {
     CausalItem it;
-    it.q0 = (tiles(g) - 1) * kT;
+    seek(g);
+    it.q0 = place * kT;
     const int idx = g - s.first[place];
     int sq;
     if (idx < (1 << 23)) {              // exact in fp32, the quotient off by at most one
@@ -118,28 +131,27 @@ struct Walk {
     }
     it.b = s.perm[sq];
     it.h = idx - sq * s.nh;
-    it.c0 = s.cu[it.b];
-    it.len = s.cu[it.b + 1] - it.c0;
+    it.c0 = __ldg(s.cu + it.b);
+    it.len = __ldg(s.cu + it.b + 1) - it.c0;
     return it;
   }
 };
 
-// Builds the list (all threads).  False: the CTA must quit (error word set, or bad bounds, which are recorded).
+// Builds the list (all threads) at `base`, with classes + 1 words at `cursor` for the time of the call.
+// False: the CTA must quit (error word set, or bad bounds, which are recorded).
 __device__ __forceinline__ bool build_list(const int32_t* __restrict__ cu, int B, int T_max, int max_len, int nh,
-                                           int classes, int32_t* err, int* s_status, uint8_t* base, List& out) {
-  int* s_cu = reinterpret_cast<int*>(base);
-  int16_t* perm = reinterpret_cast<int16_t*>(base + (static_cast<uint32_t>(B + 1) * 4u + 15u) / 16u * 16u);
-  int* first = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(perm) +
-                                      (static_cast<uint32_t>(B) * 2u + 15u) / 16u * 16u);
-  int* cursor = first + classes + 2;    // [classes + 1]: by number of items: count, then next position in perm
+                                           int classes, int32_t* err, int* s_status, uint8_t* base, int* cursor,
+                                           List& out) {
+  int16_t* perm = reinterpret_cast<int16_t*>(base);
+  int* first = reinterpret_cast<int*>(base + perm_bytes(B));
+  // cursor[c], c = 1 .. classes: sequences of c items, then the next position of one in perm
   if (threadIdx.x == 0) *s_status = device_error_set(err) ? -1 : 0;
   for (int c = threadIdx.x; c <= classes; c += blockDim.x) cursor[c] = 0;
-  for (int b = threadIdx.x; b <= B; b += blockDim.x) s_cu[b] = __ldg(cu + b);
   __syncthreads();
   if (*s_status) return false;
   __syncthreads();
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int c0 = s_cu[b], c1 = s_cu[b + 1];
+    const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
     const long long len = static_cast<long long>(c1) - c0;
     if (c0 < 0 || len < 0 || c1 > T_max || len > max_len) {
       atomicCAS(s_status, 0, len > max_len ? RPP_DERR_LENGTH : RPP_DERR_ROWS);
@@ -169,7 +181,7 @@ __device__ __forceinline__ bool build_list(const int32_t* __restrict__ cu, int B
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int b = b0 + lane;
       int c = 0;
-      if (b < B) c = (s_cu[b + 1] - s_cu[b] + kT - 1) / kT;
+      if (b < B) c = (__ldg(cu + b + 1) - __ldg(cu + b) + kT - 1) / kT;
       const unsigned peers = __match_any_sync(0xffffffffu, c);
       const int rank = __popc(peers & ((1u << lane) - 1u));
       if (c > 0) perm[cursor[c] + rank] = static_cast<int16_t>(b);
@@ -179,7 +191,7 @@ __device__ __forceinline__ bool build_list(const int32_t* __restrict__ cu, int B
     }
   }
   __syncthreads();
-  out = List{s_cu, perm, first, classes, nh, first[classes], __frcp_rn(static_cast<float>(nh))};
+  out = List{cu, perm, first, classes, nh, first[classes], __frcp_rn(static_cast<float>(nh))};
   return true;
 }
 
@@ -205,6 +217,11 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   return w & ~((f & 0x8000u ? 0xffffu : 0u) | (f & 0x80000000u ? 0xffff0000u : 0u));
 }
 
+__device__ __forceinline__ bool elect_one() {   // one lane of a converged warp
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -237,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* o_full = bars + 17;                    // the item's last PV is done
   uint64_t* o_free = bars + 18;                    // O read out by the four warps
   uint64_t* drain = bars + 19;
+  uint64_t* v_ready = bars + 20;                   // [kSlots] a V tile has landed and been looked over
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   int* s_status = reinterpret_cast<int*>(smem + S::kOffMisc + 8);
@@ -251,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&v_ready[i], 2);
     }
     for (int i = 0; i < S::kQ; ++i) {
       mbar_init(&q_full[i], 1);
@@ -270,152 +289,227 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tv);
   }
   List list;
-  if (!build_list(cu, B, T_max, max_len, nh, classes, err, s_status, smem + S::kOffList, list)) return;
+  // (the list's scratch words lie where the tiles will be)
+  if (!build_list(cu, B, T_max, max_len, nh, classes, err, s_status, smem + S::kOffList, reinterpret_cast<int*>(smem),
+                  list))
+    return;
   if (item_of_round(0, list.total) < 0) return;    // the whole CTA; nothing allocated yet
   if (warp == 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  fence_proxy_async_smem();   // the list's scratch words come before the tiles that TMA writes there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Registers: 2 CTAs x 256 threads launch with 128 each, 32768 a CTA; 128 x 64 + 128 x 192 is that sum.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      uint32_t idx = 0, nq = 0;                    // ring tiles and Q tiles issued
-      bool ok = true;
-      auto load = [&](const CUtensorMap* map, int col, int row) -> bool {
-        const uint32_t s = idx % S::kSlots;
-        if (!mbar_wait_bounded(&empty[s], ((idx / S::kSlots) & 1u) ^ 1u, abort_flag)) return false;
-        mbar_arrive_expect_tx(&full[s], S::kTileBytes);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        uint32_t idx = 0, nq = 0;                    // ring tiles and Q tiles issued
+        bool ok = true;
+        auto load = [&](const CUtensorMap* map, int col, int row) -> bool {
+          const uint32_t s = idx % S::kSlots;
+          if (!mbar_wait_bounded(&empty[s], ((idx / S::kSlots) & 1u) ^ 1u, abort_flag)) return false;
+          mbar_arrive_expect_tx(&full[s], S::kTileBytes);
 #pragma unroll
-        for (int c = 0; c < HB; ++c)
-          tma_load_2d(ring + s * S::kTileBytes + c * kBox, map, &full[s], col + 64 * c, row);
-        ++idx;
-        return true;
-      };
+          for (int c = 0; c < HB; ++c)
+            tma_load_2d(ring + s * S::kTileBytes + c * kBox, map, &full[s], col + 64 * c, row);
+          ++idx;
+          return true;
+        };
+        Walk walk(list);
+        for (int r = 0; ok; ++r) {
+          const int g = item_of_round(r, list.total);
+          if (g < 0) break;
+          const CausalItem it = walk.at(g);
+          const int kv_col = it.h / group * D;
+          const int n = it.tiles();
+          const uint32_t b = nq % S::kQ;
+          if (!mbar_wait_bounded(&q_empty[b], ((nq / S::kQ) & 1u) ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&q_full[b], S::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < HB; ++c)
+            tma_load_2d(sQ + b * S::kTileBytes + c * kBox, &tq, &q_full[b], q_x + it.h * D + 64 * c, it.c0 + it.q0);
+          ++nq;
+          for (int j = 0; j < n && ok; ++j)
+            ok = load(&tk, k_x + kv_col, it.c0 + j * kT) && load(&tv, v_x + kv_col, it.c0 + j * kT);
+        }
+        if (!ok) {
+          set_device_error(err, RPP_DERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        // what is in flight lands before the CTA can exit: the last load of each buffer
+        for (uint32_t i = idx > S::kSlots ? idx - S::kSlots : 0; i < idx; ++i)
+          mbar_wait_bounded(&full[i % S::kSlots], (i / S::kSlots) & 1u, nullptr);
+        for (uint32_t i = nq > S::kQ ? nq - S::kQ : 0; i < nq; ++i)
+          mbar_wait_bounded(&q_full[i % S::kQ], (i / S::kQ) & 1u, nullptr);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the loop and one elected lane issues, so that descriptors stay in uniform
+      // registers: from a branch of one lane each product took 70 to 80 cycles to issue.
+      {
+        const bool leader = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+          const int w = mbar_wait_bounded(bar, parity, abort_flag) ? 1 : 0;
+          return __all_sync(0xffffffffu, w) != 0;
+        };
+        constexpr int fmt = attn::Fmt<T>::v;
+        constexpr uint32_t IDESC_S = idesc_f16(fmt, kT, kT);
+        constexpr uint32_t IDESC_O = idesc_f16(fmt, kT, D) | (1u << 16);   // B (= V) N-major
+        // V: N-major, 64 columns a box (the second box kBox further), 8 keys 1024 bytes apart
+        constexpr uint64_t kVLead = D == 128 ? (static_cast<uint64_t>(kBox >> 4) << 16) - (1ull << 16) : 0ull;
+        uint32_t ns = 0, np = 0, nq = 0, no = 0;     // S and PV issued, items whose S / PV are all issued
+        bool ok = true;
+        // the next S of the line of tiles: tile j of n of its item
+        auto issue_s = [&](int j, int n) -> bool {
+          const uint32_t i = 2u * ns, s = i % S::kSlots, b = nq % S::kQ;
+          if (j == 0 && !wait(&q_full[b], (nq / S::kQ) & 1u)) return false;
+          if (!wait(&full[s], (i / S::kSlots) & 1u)) return false;
+          if (S::kApart && ns && !wait(s_free, (ns - 1) & 1u)) return false;
+          tc_fence_after();
+          const uint32_t qa = smem_u32(sQ + b * S::kTileBytes), ka = smem_u32(ring + s * S::kTileBytes);
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc_mma_f16(tmem, sw128_kmajor_desc(qa + (k >> 2) * kBox) + 2u * (k & 3),
+                         sw128_kmajor_desc(ka + (k >> 2) * kBox) + 2u * (k & 3), IDESC_S, k ? 1u : 0u);
+            tc_commit(s_full);
+            tc_commit(&empty[s]);
+            if (j == n - 1) tc_commit(&q_empty[b]);
+          }
+          __syncwarp();
+          ++ns;
+          if (j == n - 1) ++nq;
+          return true;
+        };
+        auto issue_pv = [&](int j, int n) -> bool {
+          const uint32_t s = (2u * np + 1u) % S::kSlots;
+          if (!wait(&v_ready[s], (np / S::kVSlots) & 1u)) return false;
+          if (j == 0 && no && !wait(o_free, (no - 1) & 1u)) return false;
+          const uint64_t vd = sw128_kmajor_desc(smem_u32(ring + s * S::kTileBytes)) + kVLead;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(&p_half[h], np & 1u)) return false;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)   // 16 keys: P columns +8, V +2048 bytes
+                tc_mma_f16_tmem_a(tmem + S::kColO, tmem + S::kColP + 8u * k, vd + 128u * k, IDESC_O,
+                                  (j | k) ? 1u : 0u);
+            }
+            __syncwarp();
+          }
+          if (leader) {
+            tc_commit(&empty[s]);
+            if (S::kApart) tc_commit(pv_done);
+            if (j == n - 1) tc_commit(o_full);
+          }
+          __syncwarp();
+          ++np;
+          if (j == n - 1) ++no;
+          return true;
+        };
+        // one line of tiles over this CTA's items; S runs one tile ahead of PV
+        Walk walk(list);
+        int rs = 0, js = 0, n_s = walk.tiles(item_of_round(0, list.total));
+        int jp = 0, n_p = n_s;
+        bool more = true;
+        ok = issue_s(0, n_s);
+        while (ok) {
+          // the tile after the one S was issued for last
+          int j2 = js + 1, n2 = n_s;
+          if (j2 == n_s) {
+            const int g = item_of_round(++rs, list.total);
+            more = g >= 0;
+            j2 = 0;
+            if (more) n2 = walk.tiles(g);
+          }
+          if (S::kApart) {
+            ok = (!more || issue_s(j2, n2)) && issue_pv(jp, n_p);
+          } else {
+            ok = issue_pv(jp, n_p) && (!more || issue_s(j2, n2));
+          }
+          if (!more) break;
+          jp = js = j2;
+          n_p = n_s = n2;
+        }
+        if (!ok && leader) {
+          set_device_error(err, RPP_DERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        if (leader) tc_commit(drain);                // every MMA done before tensor memory is freed
+        __syncwarp();
+        mbar_wait_bounded(drain, 0, nullptr);
+      }
+    } else {
+      // ------------------------------------------------------------ V: what some queries must not see
+      // Every V tile passes here on its way to the product.  In a tile that reaches past the
+      // item's first query, rows past the sequence become zero, and elements that are not finite
+      // are taken out and the fact noted for good.
+      const int t = (warp - 2) * 32 + lane;
+      uint32_t nv = 0;                               // V tiles passed
+      bool ok = true;
       Walk walk(list);
       for (int r = 0; ok; ++r) {
         const int g = item_of_round(r, list.total);
         if (g < 0) break;
         const CausalItem it = walk.at(g);
-        const int kv_col = it.h / group * D;
-        const int n = it.q0 / kT + 1;
-        const uint32_t b = nq % S::kQ;
-        if (!mbar_wait_bounded(&q_empty[b], ((nq / S::kQ) & 1u) ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(&q_full[b], S::kTileBytes);
+        const int n = it.tiles();
+        for (int j = 0; j < n; ++j, ++nv) {
+          const uint32_t i = 2u * nv + 1u, s = i % S::kSlots;
+          const int w = mbar_wait_bounded(&full[s], (i / S::kSlots) & 1u, abort_flag) ? 1 : 0;
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          if (j == n - 1) {
+#pragma unroll 1
+            for (int row = t; row < kT; row += 64) {
+              uint8_t* vrow = ring + s * S::kTileBytes + row * 128;
+              auto chunk = [&](int c) {
+                return reinterpret_cast<uint4*>(vrow + (c >> 3) * kBox + ((c & 7) ^ (row & 7)) * 16);
+              };
+              if (j * kT + row >= it.len) {
 #pragma unroll
-        for (int c = 0; c < HB; ++c)
-          tma_load_2d(sQ + b * S::kTileBytes + c * kBox, &tq, &q_full[b], q_x + it.h * D + 64 * c, it.c0 + it.q0);
-        ++nq;
-        for (int j = 0; j < n && ok; ++j)
-          ok = load(&tk, k_x + kv_col, it.c0 + j * kT) && load(&tv, v_x + kv_col, it.c0 + j * kT);
+                for (int c = 0; c < HB * 8; ++c) *chunk(c) = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                uint32_t f = 0;
+#pragma unroll 4
+                for (int c = 0; c < HB * 8; ++c) {
+                  const uint4 x = *chunk(c);
+                  f |= nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w);
+                }
+                if (f & 0x80008000u) {
+                  *met = 1;
+#pragma unroll 1
+                  for (int c = 0; c < HB * 8; ++c) {
+                    const uint4 x = *chunk(c);
+                    *chunk(c) = make_uint4(finite2<T>(x.x), finite2<T>(x.y), finite2<T>(x.z), finite2<T>(x.w));
+                  }
+                }
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_ready[s]);
+        }
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_device_error(err, RPP_DERR_TIMEOUT);
         *abort_flag = 1;
       }
-      // what is in flight lands before the CTA can exit: the last load of each buffer
-      for (uint32_t i = idx > S::kSlots ? idx - S::kSlots : 0; i < idx; ++i)
-        mbar_wait_bounded(&full[i % S::kSlots], (i / S::kSlots) & 1u, nullptr);
-      for (uint32_t i = nq > S::kQ ? nq - S::kQ : 0; i < nq; ++i)
-        mbar_wait_bounded(&q_full[i % S::kQ], (i / S::kQ) & 1u, nullptr);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr int fmt = attn::Fmt<T>::v;
-      constexpr uint32_t IDESC_S = idesc_f16(fmt, kT, kT);
-      constexpr uint32_t IDESC_O = idesc_f16(fmt, kT, D) | (1u << 16);   // B (= V) N-major
-      // V: N-major, 64 columns a box (the second box kBox further), 8 keys 1024 bytes apart
-      constexpr uint64_t kVLead = D == 128 ? (static_cast<uint64_t>(kBox >> 4) << 16) - (1ull << 16) : 0ull;
-      uint32_t ns = 0, np = 0, nq = 0, no = 0;     // S and PV issued, items whose S / PV are all issued
-      bool ok = true;
-      // the next S of the line of tiles: tile j of n of its item
-      auto issue_s = [&](int j, int n) -> bool {
-        const uint32_t i = 2u * ns, s = i % S::kSlots, b = nq % S::kQ;
-        if (j == 0 && !mbar_wait_bounded(&q_full[b], (nq / S::kQ) & 1u, abort_flag)) return false;
-        if (!mbar_wait_bounded(&full[s], (i / S::kSlots) & 1u, abort_flag)) return false;
-        if (S::kApart && ns && !mbar_wait_bounded(s_free, (ns - 1) & 1u, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t qa = smem_u32(sQ + b * S::kTileBytes), ka = smem_u32(ring + s * S::kTileBytes);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_f16(tmem, sw128_kmajor_desc(qa + (k >> 2) * kBox) + 2u * (k & 3),
-                     sw128_kmajor_desc(ka + (k >> 2) * kBox) + 2u * (k & 3), IDESC_S, k ? 1u : 0u);
-        tc_commit(s_full);
-        tc_commit(&empty[s]);
-        ++ns;
-        if (j == n - 1) {
-          tc_commit(&q_empty[b]);
-          ++nq;
-        }
-        return true;
-      };
-      auto issue_pv = [&](int j, int n) -> bool {
-        const uint32_t i = 2u * np + 1u, s = i % S::kSlots;
-        if (!mbar_wait_bounded(&full[s], (i / S::kSlots) & 1u, abort_flag)) return false;
-        if (j == 0 && no && !mbar_wait_bounded(o_free, (no - 1) & 1u, abort_flag)) return false;
-        const uint64_t vd = sw128_kmajor_desc(smem_u32(ring + s * S::kTileBytes)) + kVLead;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait_bounded(&p_half[h], np & 1u, abort_flag)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 4 * h; k < 4 * h + 4; ++k)   // 16 keys: P columns +8, V +2048 bytes
-            tc_mma_f16_tmem_a(tmem + S::kColO, tmem + S::kColP + 8u * k, vd + 128u * k, IDESC_O, (j | k) ? 1u : 0u);
-        }
-        tc_commit(&empty[s]);
-        if (S::kApart) tc_commit(pv_done);
-        ++np;
-        if (j == n - 1) {
-          tc_commit(o_full);
-          ++no;
-        }
-        return true;
-      };
-      // one line of tiles over this CTA's items; S runs one tile ahead of PV
-      Walk walk(list);
-      int rs = 0, js = 0, n_s = walk.tiles(item_of_round(0, list.total));
-      int jp = 0, n_p = n_s;
-      bool more = true;
-      ok = issue_s(0, n_s);
-      while (ok) {
-        // the tile after the one S was issued for last
-        int j2 = js + 1, n2 = n_s;
-        if (j2 == n_s) {
-          const int g = item_of_round(++rs, list.total);
-          more = g >= 0;
-          j2 = 0;
-          if (more) n2 = walk.tiles(g);
-        }
-        if (S::kApart) {
-          ok = (!more || issue_s(j2, n2)) && issue_pv(jp, n_p);
-        } else {
-          ok = issue_pv(jp, n_p) && (!more || issue_s(j2, n2));
-        }
-        if (!more) break;
-        jp = js = j2;
-        n_p = n_s = n2;
-      }
-      if (!ok) {
-        set_device_error(err, RPP_DERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      tc_commit(drain);                            // every MMA done before tensor memory is freed
-      mbar_wait_bounded(drain, 0, nullptr);
-    }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
     // ------------------------------------------------------------ softmax: one thread a query row
     const int quad = warp & 3;                     // tensor-memory lanes of this warp
     const int row = quad * 32 + lane;              // query of the tile, and V row of a diagonal tile
@@ -434,131 +528,159 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int g = item_of_round(r, list.total);
       if (g < 0) break;
       const CausalItem it = walk.at(g);
-      const int nt = it.q0 / kT + 1;
+      const int nt = it.tiles();
+      const bool live = it.q0 + quad * 32 < it.len;   // some of this warp's queries exist
       float m = neg_inf(), l = 0.f;
       for (int j = 0; j < nt; ++j) {
-        const bool diag = j == nt - 1;
-        if (diag) {
-          // this thread's V row of the diagonal tile, while S is computed: zero past the sequence;
-          // elements that are not finite are taken out, and the fact noted for good
-          const uint32_t i = 2u * ns + 1u, s = i % S::kSlots;
-          if (!wait(&full[s], (i / S::kSlots) & 1u)) {
-            ok = false;
-            break;
-          }
-          const bool past = it.q0 + row >= it.len;
-          uint8_t* vrow = ring + s * S::kTileBytes + row * 128;
-          auto chunk = [&](int c) {
-            return reinterpret_cast<uint4*>(vrow + (c >> 3) * kBox + ((c & 7) ^ (row & 7)) * 16);
-          };
-          if (past) {
-#pragma unroll
-            for (int c = 0; c < HB * 8; ++c) *chunk(c) = make_uint4(0u, 0u, 0u, 0u);
-          } else {
-            uint32_t f = 0;
-#pragma unroll
-            for (int c = 0; c < HB * 8; ++c) {
-              const uint4 w = *chunk(c);
-              f |= nonfinite2<T>(w.x) | nonfinite2<T>(w.y) | nonfinite2<T>(w.z) | nonfinite2<T>(w.w);
-            }
-            if (f & 0x80008000u) {
-              *met = 1;
-#pragma unroll 1
-              for (int c = 0; c < HB * 8; ++c) {
-                const uint4 w = *chunk(c);
-                *chunk(c) = make_uint4(finite2<T>(w.x), finite2<T>(w.y), finite2<T>(w.z), finite2<T>(w.w));
-              }
-            }
-          }
-          fence_proxy_async_smem();
-        }
+        // 32-key blocks of the tile that this warp's queries see, in the diagonal tile the last in part
+        const bool tri = j == nt - 1;
+        const int seen = !live ? 0 : tri ? quad + 1 : kT / 32;
         if (!wait(s_full, ns & 1u)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // scores: the second half on its way while the first half's maximum is taken
-        uint32_t v[128];
-        tmem_ld_32x32b_x32(t_s, v);
-        tmem_ld_32x32b_x32(t_s + 32, v + 32);
-        tmem_ld_wait_tied32(v);
-        tmem_ld_wait_tied32(v + 32);
-        tmem_ld_32x32b_x32(t_s + 64, v + 64);
-        tmem_ld_32x32b_x32(t_s + 96, v + 96);
-        float pm[4];
-        auto half_max = [&](int c) {
-          if (diag) {
-#pragma unroll
-            for (int e = 64 * c; e < 64 * c + 64; ++e)
-              if (e > row) v[e] = 0xff800000u;
-          }
-          if (c == 0) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) pm[t] = fmaxf(__uint_as_float(v[t]), __uint_as_float(v[t + 4]));
-          }
-#pragma unroll
-          for (int e = c ? 64 : 8; e < 64 * c + 64; e += 8)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) pm[t] = max3(pm[t], __uint_as_float(v[e + t]), __uint_as_float(v[e + t + 4]));
-        };
-        half_max(0);
-        tmem_ld_wait_tied32(v + 64);
-        tmem_ld_wait_tied32(v + 96);
-        if (S::kApart) {                           // S may be overwritten
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
-        }
-        half_max(1);
-        const float mx = fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]) * scale_log2;
-        if (S::kApart && j > 0) {                  // the last PV has read P and left O
-          if (!wait(pv_done, (ns - 1) & 1u)) {
-            ok = false;
-            break;
-          }
+        uint64_t sum2[2] = {0ull, 0ull}, nm2 = 0ull;
+        // the last PV has read P and left O (P over S: s_full says so)
+        auto last_pv = [&]() -> bool {
+          if (!S::kApart || j == 0) return true;
+          if (!wait(pv_done, (ns - 1) & 1u)) return false;
           tc_fence_after();
-        }
-        // The maximum moves lazily; O may be touched as the last PV is done.  The accesses to
-        // tensor memory are the whole warp's (factor 1 for the rows that stay).
-        const bool move = mx > m + 8.0f;
-        if (j == 0) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, move)) {
-          const float alpha = move ? ex2_approx(m - mx) : 1.0f;
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t ov[16];
-            tmem_ld_32x32b_x16(t_o + 16 * c, ov);
-            tmem_ld_wait_tied16(ov);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st_32x32b_x16(t_o + 16 * c, ov);
-            tmem_st_wait_tied16(ov);
-          }
-          if (move) {
-            l *= alpha;
+          return true;
+        };
+        // Takes the tile's maximum into the row's: it moves lazily, and then O and the sum with it.
+        // The accesses to tensor memory are the whole warp's (factor 1 for the rows that stay).
+        auto take_max = [&](float mx) {
+          const bool move = mx > m + 8.0f;
+          if (j == 0) {
             m = mx;
+          } else if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? ex2_approx(m - mx) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t ov[16];
+              tmem_ld_32x32b_x16(t_o + 16 * c, ov);
+              tmem_ld_wait_tied16(ov);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st_32x32b_x16(t_o + 16 * c, ov);
+              tmem_st_wait_tied16(ov);
+            }
+            if (move) {
+              l *= alpha;
+              m = mx;
+            }
           }
-        }
-        // scores all -inf so far: weights 0, not 2^(-inf + inf)
-        const float nm = m == neg_inf() ? 0.f : -m;
-        const uint64_t nm2 = f2_pack(nm, nm);
-        uint64_t sum2[2] = {0ull, 0ull};
+          // scores all -inf so far: weights 0, not 2^(-inf + inf)
+          const float nm = m == neg_inf() ? 0.f : -m;
+          nm2 = f2_pack(nm, nm);
+        };
+        auto weights = [&](const uint32_t* sc, uint32_t* p, int n2) {   // 2 n2 scores -> n2 pairs of weights
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int a = 64 * c + 2 * e;
-            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(v[a]), __uint_as_float(v[a + 1])), sc2, nm2);
+          for (int e = 0; e < n2; ++e) {
+            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sc2, nm2);
             const float p0 = ex2_approx(f2_lo(x2)), p1 = ex2_approx(f2_hi(x2));
             sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
-            v[32 * c + e] = pack2<T>(p0, p1);
+            p[e] = pack2<T>(p0, p1);
           }
-          tmem_st_32x32b_x32(t_p + 32 * c, v + 32 * c);
-          tmem_st_wait_tied32(v + 32 * c);
+        };
+        auto part_out = [&](int c) {                  // 64 keys of P are in tensor memory
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_half[c]);
+        };
+        auto s_read = [&]() {                         // S may be overwritten
+          if (!S::kApart) return;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+        };
+        if (seen == kT / 32 && !tri) {
+          // ---- a whole tile: scores in registers, the second part on its way while the first
+          // part's maximum is taken
+          uint32_t v[kT];
+          float pm[4];
+          auto load = [&](int c) {
+            tmem_ld_32x32b_x32(t_s + 64 * c, v + 64 * c);
+            tmem_ld_32x32b_x32(t_s + 64 * c + 32, v + 64 * c + 32);
+          };
+          load(0);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld_wait_tied32(v + 64 * c);
+            tmem_ld_wait_tied32(v + 64 * c + 32);
+            if (c + 1 < 2) load(c + 1);
+            else s_read();
+            if (c == 0) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) pm[t] = fmaxf(__uint_as_float(v[t]), __uint_as_float(v[t + 4]));
+            }
+#pragma unroll
+            for (int e = c ? 64 * c : 8; e < 64 * c + 64; e += 8)
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                pm[t] = max3(pm[t], __uint_as_float(v[e + t]), __uint_as_float(v[e + t + 4]));
+          }
+          if (!last_pv()) {
+            ok = false;
+            break;
+          }
+          take_max(fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]) * scale_log2);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            weights(v + 64 * c, v + 32 * c, 32);
+            tmem_st_32x32b_x32(t_p + 32 * c, v + 32 * c);
+            tmem_st_wait_tied32(v + 32 * c);
+            part_out(c);
+          }
+        } else {
+          // ---- a tile that these queries see in part: block by block, twice (maximum, weights);
+          // blocks that none of them sees have weight 0
+          uint32_t v[32];
+          auto block = [&](int c) {
+            tmem_ld_32x32b_x32(t_s + 32 * c, v);
+            tmem_ld_wait_tied32(v);
+            if (tri && c == seen - 1) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e > lane) v[e] = 0xff800000u;
+            }
+          };
+          float mx = neg_inf();
+#pragma unroll 1
+          for (int c = 0; c < seen; ++c) {
+            block(c);
+            float pm[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) pm[t] = fmaxf(__uint_as_float(v[t]), __uint_as_float(v[t + 4]));
+#pragma unroll
+            for (int e = 8; e < 32; e += 8)
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                pm[t] = max3(pm[t], __uint_as_float(v[e + t]), __uint_as_float(v[e + t + 4]));
+            mx = fmaxf(mx, fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]));
+          }
+          if (!last_pv()) {
+            ok = false;
+            break;
+          }
+          if (seen > 0) take_max(mx * scale_log2);
+#pragma unroll 1
+          for (int c = 0; c < kT / 32; ++c) {
+            if (c < seen) {
+              block(c);
+              weights(v, v, 16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = 0u;
+            }
+            if (live) {
+              tmem_st_32x32b_x16(t_p + 16 * c, v);
+              tmem_st_wait_tied16(v);
+            }
+            if (c == kT / 32 - 1) s_read();
+            if (c & 1) part_out(c >> 1);
+          }
         }
         l += (f2_lo(sum2[0]) + f2_hi(sum2[0])) + (f2_lo(sum2[1]) + f2_hi(sum2[1]));
         ++ns;
@@ -580,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(o_free);
       const float inv = 1.0f / l;
       // Elements that were taken out of the diagonal tile are added back from memory to the rows
-      // that see them.  (The note is visible here: o_full came after the p_half of that tile.)
+      // that see them.  (The note is visible here: o_full came after the v_ready of that tile.)
       if (*met != 0 && it.q0 + row < it.len) {
         for (int k = it.q0; k <= it.q0 + row; ++k) {
           const T* vr = v_rows + static_cast<long long>(it.c0 + k) * kv_stride + it.h / group * D;
@@ -647,8 +769,8 @@ cudaError_t launch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
   const int classes = (a.max_len + kT - 1) / kT;
   const size_t smem = 1024 + S::kOffList + list_bytes(a.B, classes);
   static SmemLimit limit;
-  const cudaError_t e =
-      limit.raise(attention_causal_kernel<T, D>, 1024 + S::kOffList + list_bytes(kMaxPrompts, kMaxCausalLen / kT));
+  const cudaError_t e = limit.raise(
+      attention_causal_kernel<T, D>, 1024 + S::kOffList + list_bytes(kMaxPrompts, kMaxCausalLen / kT), kLaunchRegs);
   if (e != cudaSuccess) return e;
   // never more CTAs than items: ceil(len / 128) <= len / 128 + 1 for each sequence
   const long long most = (static_cast<long long>(a.T_max) / kT + a.B) * a.nh;
@@ -681,17 +803,18 @@ cudaError_t launch_attention_causal(const CausalArgs& a, cudaStream_t stream) {
   const uintptr_t first = std::min(q, std::min(k, v));
   const uintptr_t end = std::max(q + 2u * static_cast<uintptr_t>(a.nh) * a.d,
                                  std::max(k, v) + 2u * static_cast<uintptr_t>(a.nkv) * a.d);
+  auto map = [&](CUtensorMap* m, const void* base, int cols, int stride) {
+    return make_tmap_2d(m, base, dt, 2, a.T_max, cols, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, stride);
+  };
   if (a.q_stride == a.kv_stride && end - first <= 2u * static_cast<uintptr_t>(a.q_stride)) {
-    if (!make_tmap_2d(&t.q, reinterpret_cast<const void*>(first), dt, 2, a.T_max, static_cast<int>((end - first) / 2),
-                      kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.q_stride))
+    if (!map(&t.q, reinterpret_cast<const void*>(first), static_cast<int>((end - first) / 2), a.q_stride))
       return cudaErrorInvalidValue;
     t.k = t.v = t.q;
     t.q_x = static_cast<int>((q - first) / 2);
     t.k_x = static_cast<int>((k - first) / 2);
     t.v_x = static_cast<int>((v - first) / 2);
-  } else if (!make_tmap_2d(&t.q, a.q, dt, 2, a.T_max, a.nh * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.q_stride) ||
-             !make_tmap_2d(&t.k, a.k, dt, 2, a.T_max, a.nkv * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.kv_stride) ||
-             !make_tmap_2d(&t.v, a.v, dt, 2, a.T_max, a.nkv * a.d, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, a.kv_stride)) {
+  } else if (!map(&t.q, a.q, a.nh * a.d, a.q_stride) || !map(&t.k, a.k, a.nkv * a.d, a.kv_stride) ||
+             !map(&t.v, a.v, a.nkv * a.d, a.kv_stride)) {
     return cudaErrorInvalidValue;
   }
   return a.dtype == RPP_F16 ? dispatch<__half>(t, a, stream) : dispatch<__nv_bfloat16>(t, a, stream);

@@ -11,16 +11,23 @@ int num_sms();   // SM count of the current device (cached per device)
 
 // Raises a kernel's dynamic shared memory limit on the current device, once per device (the
 // attribute is the device's, and setting it costs a part of a launch).  Two callers at once may
-// both set it, to the same value.
+// both set it, to the same value.  `regs`, if given: the registers a thread that the kernel must have
+// been compiled to (kernels that split them between their warps count on it).
 struct SmemLimit {
   std::atomic<bool> set[64] = {};
   template <typename K>
-  cudaError_t raise(K* kernel, size_t bytes) {
+  cudaError_t raise(K* kernel, size_t bytes, int regs = 0) {
     int dev = -1;
     const cudaError_t g = cudaGetDevice(&dev);
     if (g != cudaSuccess) return g;
     const bool known = dev >= 0 && dev < 64;
     if (known && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    if (regs) {
+      cudaFuncAttributes a;
+      const cudaError_t q = cudaFuncGetAttributes(&a, kernel);
+      if (q != cudaSuccess) return q;
+      if (a.numRegs != regs) return cudaErrorInvalidDeviceFunction;
+    }
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e == cudaSuccess && known) set[dev].store(true, std::memory_order_release);

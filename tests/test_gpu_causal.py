@@ -235,3 +235,18 @@ def test_q_k_and_v_as_tensors_of_their_own(d):
     for a in ((q.contiguous(), k.contiguous(), v.contiguous()), (q, kv[:, nkv * d:], kv[:, :nkv * d]),
               (q.contiguous(), kv[:, nkv * d:], kv[:, :nkv * d])):
         assert torch.equal(rpp.attention_causal_varlen(*a, ints(cu_of(lens)), 3, 300, nh, nkv, d), want)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_ragged_batch_many_times(dtype, d):
+    """Items whose last queries do not exist next to full ones, several to a CTA, one launch after the other: every
+    run the same, and right.  (Warps without queries run ahead of the others here.)"""
+    lens, nh, nkv = [1, 0, 300, 128, 5, 129, 0, 256, 77, 257, 640, 2, 0] * 3, 32, 8
+    q, k, v = make(lens, nh, nkv, d, dtype, seed=32)
+    cu, err = cu_of(lens), rpp.new_error_word()
+    outs = [rpp.attention_causal_varlen(q, k, v, ints(cu), len(lens), 640, nh, nkv, d, err=err) for _ in range(40)]
+    assert rpp.get_device_error(err) == 0
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    check_rows(outs[0], q, k, v, cu, nh, nkv, d, seqs=range(13), heads=[0, 13, 31])
