@@ -70,8 +70,8 @@ struct Shape {
 constexpr int kThreads = 256;            // warps 0-3: TMA, MMA, V's watch; warps 4-7: softmax
 constexpr uint32_t kTmemCols = 256;
 // Registers: launched with 128 a thread, 32768 a CTA (checked at the first launch: a split above
-// what the launch has would wait for ever); 128 threads keep 64, the softmax's 128 take 192.
-constexpr int kLaunchRegs = 128, kLowRegs = 64, kHighRegs = 192;
+// what the launch has would wait for ever); 128 threads keep 80, the softmax's 128 take 176.
+constexpr int kLaunchRegs = 128, kLowRegs = 80, kHighRegs = 176;
 static_assert(128 * (kLowRegs + kHighRegs) == kLaunchRegs * kThreads, "the split must be the launch's registers");
 
 // The item list: in shared memory the sequences by falling number of items and, for each place i
@@ -368,13 +368,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         constexpr uint64_t kVLead = D == 128 ? (static_cast<uint64_t>(kBox >> 4) << 16) - (1ull << 16) : 0ull;
         uint32_t ns = 0, np = 0, nq = 0, no = 0;     // S and PV issued, items whose S / PV are all issued
         bool ok = true;
-        // the next S of the line of tiles: tile j of n of its item
-        auto issue_s = [&](int j, int n) -> bool {
-          const uint32_t i = 2u * ns, s = i % S::kSlots, b = nq % S::kQ;
-          if (j == 0 && !wait(&q_full[b], (nq / S::kQ) & 1u)) return false;
-          if (!wait(&full[s], (i / S::kSlots) & 1u)) return false;
-          if (S::kApart && ns && !wait(s_free, (ns - 1) & 1u)) return false;
-          tc_fence_after();
+        // A wait costs some 150 cycles even when there is nothing to wait for, so those for tiles that
+        // came long ago are done while the softmax runs (the *_ready calls), and between its
+        // signal and the products there is one wait.
+        auto s_ready = [&](int j) -> bool {          // operands of the next S: tile j of its item
+          const uint32_t i = 2u * ns, b = nq % S::kQ;
+          return (j || wait(&q_full[b], (nq / S::kQ) & 1u)) && wait(&full[i % S::kSlots], (i / S::kSlots) & 1u);
+        };
+        auto do_s = [&](int j, int n) {
+          const uint32_t s = 2u * ns % S::kSlots, b = nq % S::kQ;
           const uint32_t qa = smem_u32(sQ + b * S::kTileBytes), ka = smem_u32(ring + s * S::kTileBytes);
           if (leader) {
 #pragma unroll
@@ -388,12 +390,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           __syncwarp();
           ++ns;
           if (j == n - 1) ++nq;
-          return true;
         };
-        auto issue_pv = [&](int j, int n) -> bool {
+        auto pv_ready = [&](int j) -> bool {         // operands of the next PV but P, and its O
+          return wait(&v_ready[(2u * np + 1u) % S::kSlots], (np / S::kVSlots) & 1u) &&
+                 (j || !no || wait(o_free, (no - 1) & 1u));
+        };
+        auto do_pv = [&](int j, int n) -> bool {
           const uint32_t s = (2u * np + 1u) % S::kSlots;
-          if (!wait(&v_ready[s], (np / S::kVSlots) & 1u)) return false;
-          if (j == 0 && no && !wait(o_free, (no - 1) & 1u)) return false;
           const uint64_t vd = sw128_kmajor_desc(smem_u32(ring + s * S::kTileBytes)) + kVLead;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -404,15 +407,14 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int k = 4 * h; k < 4 * h + 4; ++k)   // 16 keys: P columns +8, V +2048 bytes
                 tc_mma_f16_tmem_a(tmem + S::kColO, tmem + S::kColP + 8u * k, vd + 128u * k, IDESC_O,
                                   (j | k) ? 1u : 0u);
+              if (h) {
+                tc_commit(&empty[s]);
+                if (S::kApart) tc_commit(pv_done);
+                if (j == n - 1) tc_commit(o_full);
+              }
             }
             __syncwarp();
           }
-          if (leader) {
-            tc_commit(&empty[s]);
-            if (S::kApart) tc_commit(pv_done);
-            if (j == n - 1) tc_commit(o_full);
-          }
-          __syncwarp();
           ++np;
           if (j == n - 1) ++no;
           return true;
@@ -422,7 +424,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         int rs = 0, js = 0, n_s = walk.tiles(item_of_round(0, list.total));
         int jp = 0, n_p = n_s;
         bool more = true;
-        ok = issue_s(0, n_s);
+        ok = s_ready(0);
+        if (ok) {
+          tc_fence_after();
+          do_s(0, n_s);
+        }
         while (ok) {
           // the tile after the one S was issued for last
           int j2 = js + 1, n2 = n_s;
@@ -432,11 +438,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             j2 = 0;
             if (more) n2 = walk.tiles(g);
           }
-          if (S::kApart) {
-            ok = (!more || issue_s(j2, n2)) && issue_pv(jp, n_p);
-          } else {
-            ok = issue_pv(jp, n_p) && (!more || issue_s(j2, n2));
+          ok = (!more || s_ready(j2)) && pv_ready(jp);
+          if (S::kApart && more) {
+            ok = ok && wait(s_free, (ns - 1) & 1u);
+            if (ok) {
+              tc_fence_after();
+              do_s(j2, n2);
+            }
           }
+          ok = ok && do_pv(jp, n_p);
+          if (!S::kApart && more && ok) do_s(j2, n2);
           if (!more) break;
           jp = js = j2;
           n_p = n_s = n2;
@@ -524,10 +535,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       return __all_sync(0xffffffffu, w) != 0;
     };
     Walk walk(list);
-    for (int r = 0; ok; ++r) {
-      const int g = item_of_round(r, list.total);
-      if (g < 0) break;
-      const CausalItem it = walk.at(g);
+    int g = item_of_round(0, list.total);            // >= 0 here
+    CausalItem it = walk.at(g), nx = it;
+    for (int r = 1; g >= 0; ++r, it = nx) {
       const int nt = it.tiles();
       const bool live = it.q0 + quad * 32 < it.len;   // some of this warp's queries exist
       float m = neg_inf(), l = 0.f;
@@ -685,6 +695,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         l += (f2_lo(sum2[0]) + f2_hi(sum2[0])) + (f2_lo(sum2[1]) + f2_hi(sum2[1]));
         ++ns;
       }
+      g = item_of_round(r, list.total);
+      if (g >= 0) nx = walk.at(g);                   // while the last PV runs
       if (!ok || !wait(o_full, no & 1u)) {
         ok = false;
         break;
@@ -700,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      const float inv = 1.0f / l;
+      const float inv = __fdividef(1.0f, l);
       // Elements that were taken out of the diagonal tile are added back from memory to the rows
       // that see them.  (The note is visible here: o_full came after the v_ready of that tile.)
       if (*met != 0 && it.q0 + row < it.len) {
@@ -716,8 +728,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       // A thread has a row, a store wants whole lines: 32 columns at a time through 2 KB of shared
       // memory of the warp's own (16-byte chunk u of row r at u ^ (r / 2 & 3): no bank conflict
       // either way), then four lanes a row.
-      T* obase = out + static_cast<long long>(it.c0 + it.q0 + quad * 32) * (static_cast<long long>(nh) * D) + it.h * D;
-      const int rows_left = it.len - it.q0 - quad * 32;
+      const long long pitch = static_cast<long long>(nh) * D;
+      const int rr = lane >> 2, ch = lane & 3;         // row of an 8-row group and chunk that this lane stores
+      T* obase = out + (it.c0 + it.q0 + quad * 32 + rr) * pitch + it.h * D + 8 * ch;
+      const int rows_left = it.len - it.q0 - quad * 32 - rr;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint8_t* mine = stage + lane * 64;
@@ -733,11 +747,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int rr = 8 * u + (lane >> 2), ch = lane & 3;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
-          if (rr < rows_left)
-            *reinterpret_cast<uint4*>(obase + static_cast<long long>(rr) * (static_cast<long long>(nh) * D) + 32 * c +
-                                      8 * ch) = w;
+          // (row 8 u + rr: its swizzle is that of rr, 8 u / 2 being a multiple of 4)
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + (8 * u + rr) * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+          if (8 * u < rows_left) *reinterpret_cast<uint4*>(obase + 8 * u * pitch + 32 * c) = w;
         }
         __syncwarp();
       }
