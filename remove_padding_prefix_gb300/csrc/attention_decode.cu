@@ -22,8 +22,9 @@
 //    keeps about 16 bits of P: the second mma costs nothing while HBM is the bound.
 //  * A (sequence, kv head) that one warp had whole is written at once.  Of one that was cut
 //    each warp leaves maximum, sum and unnormalised output in the workspace, and a second
-//    kernel (programmatic launch) joins the pieces in a fixed order: results do not
-//    depend on timing.
+//    kernel (programmatic launch) joins the pieces in a fixed order: results do not depend on
+//    timing.  It has a CTA for each query head while they are few (few units of many pieces),
+//    else one for each place where the line was cut (many units of few pieces).
 //
 // Rows past the sequence are filled with zeros in shared memory (never read), so pool
 // pages may hold anything there.
@@ -40,7 +41,8 @@ constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;       // K then V, 4 KB each
 constexpr int kMinBlocks = 2;           // blocks a warp takes at least, while there are that many
 constexpr int kRows = 16;               // query heads of one product
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 128;        // join by cuts
+constexpr int kHeadThreads = 256;        // join by heads
 constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes;
 
 struct DecodeParams {
@@ -57,6 +59,7 @@ struct DecodeParams {
   float scale_log2;
   void* out;
   long long* prefix;         // [n + 1]: key blocks before each sequence (per kv head part)
+  int4* cuts;                // [warps]: where a share starts inside a unit, (sequence, unit, block in it); else -1
   float2* ml;                // [2 * warps][16]: maximum, sum
   float* acc;                // [2 * warps][min(group, 16)][d]
   int32_t* err;
@@ -148,7 +151,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
   const int warp = warp_id(), lane = lane_id();
   pdl_wait();
   pdl_trigger();
+  // one reading of the error word for the whole CTA, on its way together with the first lengths
   if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
+  int slot0;
+  const int len0 = static_cast<int>(threadIdx.x) < p.n ? seq_len(p, threadIdx.x, &slot0) : 0;
   __syncthreads();
   if (s_flag) return;
 
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
     long long v = 0;
     if (i < p.n) {
       int slot;
-      v = (seq_len(p, i, &slot) + KB - 1) / KB;
+      v = ((base ? seq_len(p, i, &slot) : len0) + KB - 1) / KB;
     }
     long long x = v;
 #pragma unroll
@@ -183,6 +189,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
     for (int i = threadIdx.x; i <= p.n; i += kWarps * 32) p.prefix[i] = s_pre[i];
   const int per_seq = p.d.kv_heads * p.parts;    // units (kv head, 16-head part) of a sequence
   const long long total = carry * per_seq;
+  // empty sequences: zeros
+  for (int i = warp * gridDim.x + blockIdx.x; i < p.n; i += kWarps * gridDim.x) {
+    if (s_pre[i + 1] != s_pre[i]) continue;
+    uint4* row = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<long long>(i) * p.nh * D);
+    for (int e = lane; e < p.nh * (D / 8); e += 32) row[e] = make_uint4(0u, 0u, 0u, 0u);
+  }
   if (total == 0) return;
   const long long warps = share_warps(total, static_cast<long long>(gridDim.x) * kWarps);
   // consecutive shares go to different SMs: warp w of CTA c has share w * CTAs + c
@@ -229,6 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
     ld.blk = static_cast<int>(rem - static_cast<long long>(ld.unit) * ld.nb);
   }
   Cursor cc = ld;                   // the block being computed
+  if (lane == 0) p.cuts[w_id] = make_int4(ld.blk > 0 ? ld.i : -1, ld.unit, ld.blk, 0);
 
   // ---- loads: 16 bytes a lane, 8 rows-groups each of K and V
   const int ps = p.d.page_size;
@@ -467,57 +480,142 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
   }
 }
 
-// One CTA per (sequence, query head): joins the pieces of a unit that was cut, writes zeros
-// for an empty sequence, and leaves the rest (written by the main kernel) alone.
+// One CTA for each share of the line: if its start is the first cut of a unit, the CTA joins that
+// unit's pieces.  A thread has four output elements of one head and, where there are fewer of
+// those than threads, one of several groups of pieces.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_decode_join_kernel(const DecodeParams p, int main_warps) {
-  constexpr int W = kJoinThreads / 32, E = D / 32;   // warps; output elements of a lane
-  constexpr int KB = kStageBytes / (4 * D);
+__global__ void __launch_bounds__(kJoinThreads, 12)
+    attention_decode_join_cuts_kernel(const DecodeParams p, int main_warps) {
+  __shared__ int s_flag;
+  __shared__ float s_m[kRows];
+  __shared__ float4 s_o[kJoinThreads];
+  __shared__ float s_lg[kJoinThreads];
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
+  const int w = blockIdx.x;
+  const int per_seq = p.d.kv_heads * p.parts;
+  const long long total = p.prefix[p.n] * per_seq;
+  __syncthreads();
+  if (s_flag || total == 0) return;
+  const long long warps = share_warps(total, main_warps);
+  if (w == 0 || w >= warps) return;
+  const int4 cut = p.cuts[w];
+  if (cut.x < 0) return;
+  const long long b0 = share_start(total, warps, w) - cut.z;       // the unit's first block
+  const long long w0 = w - 1;
+  if (share_start(total, warps, w0) > b0) return;                   // an earlier cut is in the unit too
+  const long long nb = p.prefix[cut.x + 1] - p.prefix[cut.x];
+  const int pieces = static_cast<int>(share_of(total, warps, b0 + nb - 1) - w0 + 1);
+  const int head = cut.y / p.parts, part = cut.y - head * p.parts;
+  const int have = min(kRows, p.group - part * kRows);
+  const int kept = p.group < kRows ? p.group : kRows;
+  const long long first = 2 * w0 + (b0 > share_start(total, warps, w0) ? 1 : 0);
+  auto piece = [&](int k) { return k ? 2 * (w0 + k) : first; };
+  const int warp = warp_id(), lane = lane_id();
+  for (int r = warp; r < have; r += kJoinThreads / 32) {
+    float mx = __int_as_float(0xff800000);
+    for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, p.ml[piece(k) * kRows + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) s_m[r] = mx == __int_as_float(0xff800000) ? 0.f : mx;
+  }
+  __syncthreads();
+  constexpr int V = D / 4;
+  const int items = have * V;                                       // at most 512
+  const int groups = items < kJoinThreads ? kJoinThreads / items : 1;
+  for (int base = 0; base < items; base += kJoinThreads) {
+    const int grp = groups > 1 ? threadIdx.x / items : 0;
+    const int item = groups > 1 ? threadIdx.x - grp * items : base + threadIdx.x;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (item < items && grp < groups) {
+      const int r = item / V, v = item - r * V;
+      const float m = s_m[r];
+#pragma unroll 2
+      for (int k = grp; k < pieces; k += groups) {
+        const float2 ml = p.ml[piece(k) * kRows + r];
+        const float4 x = reinterpret_cast<const float4*>(p.acc + (piece(k) * kept + r) * D)[v];
+        const float a = ex2_approx(ml.x - m);
+        l += a * ml.y;
+        acc.x += a * x.x;
+        acc.y += a * x.y;
+        acc.z += a * x.z;
+        acc.w += a * x.w;
+      }
+    }
+    if (groups > 1) {   // the groups' sums, in their order
+      s_o[threadIdx.x] = acc;
+      s_lg[threadIdx.x] = l;
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < items) {
+        for (int q = 1; q < groups; ++q) {
+          const float4 x = s_o[q * items + threadIdx.x];
+          acc.x += x.x;
+          acc.y += x.y;
+          acc.z += x.z;
+          acc.w += x.w;
+          l += s_lg[q * items + threadIdx.x];
+        }
+      }
+    }
+    if (item < items && grp == 0) {
+      const int r = item / V, v = item - r * V;
+      T* out = static_cast<T*>(p.out) +
+               (static_cast<long long>(cut.x) * p.nh + head * p.group + part * kRows + r) * D + 4 * v;
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = from_f32<T>((&acc.x)[e] * inv);
+    }
+  }
+}
+
+// One CTA for each (sequence, query head): its warps share the pieces, a lane has D / 32 elements.
+template <typename T, int D>
+__global__ void __launch_bounds__(kHeadThreads)
+    attention_decode_join_heads_kernel(const DecodeParams p, int main_warps) {
+  constexpr int W = kHeadThreads / 32, E = D / 32;
   __shared__ int s_flag;
   __shared__ float s_m[W], s_l[W];
   __shared__ float s_o[W][D];
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
-  __syncthreads();
-  if (s_flag) return;
   const int i = blockIdx.x, h = blockIdx.y;
-  const int warp = warp_id(), lane = lane_id();
-  const long long pre = p.prefix[i];
-  const long long nb = p.prefix[i + 1] - pre;
-  T* out = static_cast<T*>(p.out) + (static_cast<long long>(i) * p.nh + h) * D;
-  if (nb == 0) {
-    for (int e = threadIdx.x; e < D; e += kJoinThreads) out[e] = from_f32<T>(0.f);
-    return;
-  }
+  const long long pre = p.prefix[i], nb = p.prefix[i + 1] - pre;
   const int per_seq = p.d.kv_heads * p.parts;
   const long long total = p.prefix[p.n] * per_seq;
+  __syncthreads();
+  if (s_flag || nb == 0) return;
+  const int warp = warp_id(), lane = lane_id();
   const long long warps = share_warps(total, main_warps);
-  const int kvh = h / p.group, in_group = h - kvh * p.group;
+  const int head = h / p.group, in_group = h - head * p.group;
   const int part = in_group / kRows, row = in_group - part * kRows;
-  const long long b0 = pre * per_seq + (static_cast<long long>(kvh) * p.parts + part) * nb;
-  const long long w0 = share_of(total, warps, b0), w1 = share_of(total, warps, b0 + nb - 1);
-  if (w0 == w1) return;
-  const int rows_kept = p.group < kRows ? p.group : kRows;
+  const long long b0 = pre * per_seq + (static_cast<long long>(head) * p.parts + part) * nb;   // the unit's first block
+  const long long w0 = share_of(total, warps, b0);
+  const int pieces = static_cast<int>(share_of(total, warps, b0 + nb - 1) - w0 + 1);
+  if (pieces == 1) return;                                          // written by the warp that had it
+  const int kept = p.group < kRows ? p.group : kRows;
   const long long first = 2 * w0 + (b0 > share_start(total, warps, w0) ? 1 : 0);
-  auto piece = [&](long long w) { return w == w0 ? first : 2 * w; };
+  auto piece = [&](int k) { return k ? 2 * (w0 + k) : first; };
   float mx = __int_as_float(0xff800000);
-  for (long long w = w0 + threadIdx.x; w <= w1; w += kJoinThreads) mx = fmaxf(mx, p.ml[piece(w) * kRows + row].x);
+  for (int k = threadIdx.x; k < pieces; k += kHeadThreads) mx = fmaxf(mx, p.ml[piece(k) * kRows + row].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) s_m[warp] = mx;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w]);
-  const float base = mx == __int_as_float(0xff800000) ? 0.f : mx;
+  const float m = mx == __int_as_float(0xff800000) ? 0.f : mx;
   float acc[E], l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (long long w = w0 + warp; w <= w1; w += W) {
-    const float2 v = p.ml[piece(w) * kRows + row];
-    const float a = ex2_approx(v.x - base);
-    const float* src = p.acc + (piece(w) * rows_kept + row) * D + lane * E;
-    l += a * v.y;
+#pragma unroll 4
+  for (int k = warp; k < pieces; k += W) {
+    const float2 ml = p.ml[piece(k) * kRows + row];
+    const float* src = p.acc + (piece(k) * kept + row) * D + lane * E;
+    const float a = ex2_approx(ml.x - m);
+    l += a * ml.y;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += a * src[e];
   }
@@ -525,16 +623,15 @@ __global__ void __launch_bounds__(kJoinThreads) attention_decode_join_kernel(con
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
   if (lane == 0) s_l[warp] = l;
   __syncthreads();
-  for (int e = threadIdx.x; e < D; e += kJoinThreads) {
+  if (threadIdx.x < D) {
     float x = 0.f, z = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      x += s_o[w][e];
+      x += s_o[w][threadIdx.x];
       z += s_l[w];
     }
-    out[e] = from_f32<T>(x / z);
+    static_cast<T*>(p.out)[(static_cast<long long>(i) * p.nh + h) * D + threadIdx.x] = from_f32<T>(x / z);
   }
-  (void)KB;
 }
 
 inline size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -550,7 +647,10 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
   const int ctas = decode_ctas();
   const cudaError_t e = launch_pdl(attention_decode_kernel<T, D>, dim3(ctas), dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attention_decode_join_kernel<T, D>, dim3(p.n, p.nh), dim3(kJoinThreads), 0, stream, p,
+  if (static_cast<long long>(p.n) * p.nh <= 4 * ctas)
+    return launch_pdl(attention_decode_join_heads_kernel<T, D>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream, p,
+                      ctas * kWarps);
+  return launch_pdl(attention_decode_join_cuts_kernel<T, D>, dim3(ctas * kWarps), dim3(kJoinThreads), 0, stream, p,
                     ctas * kWarps);
 }
 
@@ -559,7 +659,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
 size_t attention_decode_ws_bytes(int n, int nh, int nkv, int d) {
   const size_t pieces = 2 * static_cast<size_t>(decode_ctas()) * kWarps;
   const int group = nh / nkv, kept = group < kRows ? group : kRows;
-  return up256((static_cast<size_t>(n) + 1) * sizeof(long long)) + up256(pieces * kRows * sizeof(float2)) +
+  return up256((static_cast<size_t>(n) + 1) * sizeof(long long)) + up256(pieces / 2 * sizeof(int4)) +
+         up256(pieces * kRows * sizeof(float2)) +
          up256(pieces * kept * d * sizeof(float));
 }
 
@@ -585,6 +686,8 @@ cudaError_t launch_attention_decode(const KvDims& d, const KvState& c, rpp_dtype
   uint8_t* at = static_cast<uint8_t*>(ws);
   p.prefix = reinterpret_cast<long long*>(at);
   at += up256((static_cast<size_t>(n) + 1) * sizeof(long long));
+  p.cuts = reinterpret_cast<int4*>(at);
+  at += up256(pieces / 2 * sizeof(int4));
   p.ml = reinterpret_cast<float2*>(at);
   at += up256(pieces * kRows * sizeof(float2));
   p.acc = reinterpret_cast<float*>(at);
