@@ -47,25 +47,34 @@ __device__ __forceinline__ int warp_scan_incl(int v) {
   return v;
 }
 
-// Reads `slots` against the cache: false (and the error recorded by one thread) if one
-// lies outside [0, d.slots) or is given twice.  `seen`: (d.slots + 31) / 32 words of
-// shared memory, `s_bad` one more.  Every CTA of a launch that calls this comes to the
-// same answer.  Holds __syncthreads: called by all threads.
-__device__ bool check_slots(const int32_t* __restrict__ slots, int n, const KvDims& d, uint32_t* seen, int* s_bad,
-                            int32_t* err) {
-  const int words = (d.slots + 31) / 32;
-  for (int i = threadIdx.x; i < words; i += blockDim.x) seen[i] = 0u;
+// The first words of a kernel that takes a list of slots: one reading of the error word for the
+// whole CTA (other CTAs may set it at any time) and the list against the cache.  False if the CTA must
+// quit: the word is set, or a slot lies outside [0, d.slots) or is given twice (recorded by one
+// thread; every CTA of a launch comes to the same answer).  `seen`: (d.slots + 31) / 32 words of shared
+// memory, left holding the slots given; first: slots[threadIdx.x], read ahead by the caller so
+// that the readings travel together.  Holds __syncthreads: called by all threads.
+struct Gate {
+  int quit, bad;
+};
+__device__ __forceinline__ bool pass(const int32_t* __restrict__ slots, int n, int first, const KvDims& d,
+                                     uint32_t* seen, Gate* g, int32_t* err) {
+  if (threadIdx.x == 0) {
+    g->quit = device_error_set(err) ? 1 : 0;
+    g->bad = 0;
+  }
+  for (int i = threadIdx.x; i < (d.slots + 31) / 32; i += blockDim.x) seen[i] = 0u;
   __syncthreads();
+  if (g->quit) return false;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int s = slots[i];
-    if (s < 0 || s >= d.slots || ((atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u)) *s_bad = 1;
+    const int s = i == static_cast<int>(threadIdx.x) ? first : slots[i];
+    if (s < 0 || s >= d.slots || ((atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u)) g->bad = 1;
   }
   __syncthreads();
-  if (*s_bad && threadIdx.x == 0) set_device_error(err, RPP_DERR_SLOT);
-  return *s_bad == 0;
+  if (g->bad && threadIdx.x == 0) set_device_error(err, RPP_DERR_SLOT);
+  return g->bad == 0;
 }
 
-// One reading of the error word for the whole CTA (other CTAs may set it at any time).
+// One reading of the error word for the whole CTA.
 __device__ __forceinline__ bool quit(const int32_t* err, int* s_flag) {
   if (threadIdx.x == 0) *s_flag = device_error_set(err) ? 1 : 0;
   __syncthreads();
@@ -103,25 +112,37 @@ __global__ void __launch_bounds__(kPlanThreads)
                       int32_t* err) {
   extern __shared__ int32_t s_need[];
   uint32_t* seen = reinterpret_cast<uint32_t*>(s_need + n + 1);
-  __shared__ int s_flag, s_bad, s_code, s_total;
+  __shared__ int s_code, s_total;
   __shared__ int s_warp[kPlanWarps];
+  __shared__ Gate gate;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) s_bad = s_code = 0;
-  if (quit(err, &s_flag)) return;
-  if (!check_slots(slots, n, d, seen, &s_bad, err)) return;
+  if (threadIdx.x == 0) s_code = 0;
+  const int warp = warp_id(), lane = lane_id();
+  // The list and the free pages of each warp's stretch, read together with the error word.
+  const int mine_i = threadIdx.x;
+  const int first = mine_i < n ? slots[mine_i] : 0;
+  const int first_arg = mine_i < n ? counts_or_from[mine_i] : 0;
+  const int2 st = warp_stretch(d.pages);
+  int mine = 0;
+  for (int p = st.x + 4 * lane; p < st.y; p += 128) {
+    const int4 r = load_refs4(refs, p, d.pages);
+    mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+  }
+  if (!pass(slots, n, first, d, seen, &gate, err)) return;
   // pages that each sequence needs
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int s = slots[i];
+    const int s = i == mine_i ? first : slots[i];
+    const int arg = i == mine_i ? first_arg : counts_or_from[i];
     int need = 0, code = 0;
     if constexpr (kFork) {
-      const int f = counts_or_from[i];
+      const int f = arg;
       if (f < 0 || f >= d.slots || ((seen[f >> 5] >> (f & 31)) & 1u)) code = RPP_DERR_SLOT;   // no slot is both
       else if (lens[s] != 0) code = RPP_DERR_SLOT;            // a fork goes to an empty slot
       else if (!len_ok(lens[f], d)) code = RPP_DERR_LENGTH;
       else need = lens[f] % d.page_size ? 1 : 0;
     } else {
-      const int old = lens[s], add = counts_or_from[i];
+      const int old = lens[s], add = arg;
       const long long grown = static_cast<long long>(old) + add;
       if (!len_ok(old, d) || add < 0 || grown > static_cast<long long>(d.max_pages) * d.page_size) code = RPP_DERR_LENGTH;
       else need = used_pages(static_cast<int>(grown), d.page_size) - used_pages(old, d.page_size);
@@ -135,7 +156,6 @@ __global__ void __launch_bounds__(kPlanThreads)
     return;
   }
   // exclusive scan of the needs (slots are distinct, so the sum is at most slots * max_pages)
-  const int warp = warp_id(), lane = lane_id();
   int carry = 0;
   for (int base = 0; base < n; base += kPlanThreads) {
     const int i = base + threadIdx.x;
@@ -157,14 +177,6 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int total = carry;
   if (threadIdx.x == 0) s_need[n] = total;
   // free pages before each warp's stretch
-  const int2 st = warp_stretch(d.pages);
-  int mine = 0;
-  if (total > 0) {
-    for (int p = st.x + 4 * lane; p < st.y; p += 128) {
-      const int4 r = load_refs4(refs, p, d.pages);
-      mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    }
-  }
   mine = warp_sum(mine);
   if (lane == 0) s_warp[warp] = mine;
   __syncthreads();
@@ -292,12 +304,11 @@ __global__ void __launch_bounds__(kMoveThreads)
     kv_free_kernel(KvDims d, int32_t* __restrict__ table, int32_t* __restrict__ lens, int32_t* __restrict__ refs,
                    const int32_t* __restrict__ slots, int n, int32_t* err) {
   extern __shared__ uint32_t s_seen[];
-  __shared__ int s_flag, s_bad;
+  __shared__ Gate gate;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) s_bad = 0;
-  if (quit(err, &s_flag)) return;
-  if (!check_slots(slots, n, d, s_seen, &s_bad, err)) return;
+  const int first = static_cast<int>(threadIdx.x) < n ? slots[threadIdx.x] : 0;
+  if (!pass(slots, n, first, d, s_seen, &gate, err)) return;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int s = slots[i];
     const int len = lens[s];
@@ -336,18 +347,17 @@ __global__ void __launch_bounds__(kMoveThreads)
                      const uint4* __restrict__ v, int row_vec, const int32_t* __restrict__ slots,
                      const int32_t* __restrict__ cu, int n, int rows_max, int tok, int32_t* err) {
   extern __shared__ uint32_t s_seen[];
-  __shared__ int s_flag, s_bad;
+  __shared__ Gate gate;
   __shared__ long long s_at[kMaxTok];   // first vector of the row in the pool (head 0 of K), -1: none
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) s_bad = 0;
-  if (quit(err, &s_flag)) return;
+  const int first = static_cast<int>(threadIdx.x) < n ? slots[threadIdx.x] : 0;
   const int T = cu ? cu[n] : n;
+  if (!pass(slots, n, first, d, s_seen, &gate, err)) return;
   if (T < 0 || T > rows_max) {
     if (threadIdx.x == 0) set_device_error(err, RPP_DERR_ROWS);
     return;
   }
-  if (!check_slots(slots, n, d, s_seen, &s_bad, err)) return;
   const int vpr = d.head_dim / 8;
   const int head_vec = d.page_size * vpr;
   const long long page_vec = 2LL * d.kv_heads * head_vec;
