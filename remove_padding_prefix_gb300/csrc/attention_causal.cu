@@ -4,21 +4,33 @@
 // query head h with the keys and values of kv head h / (nh / nkv).
 //
 // A work item is (sequence, query head, tile of 128 queries), run against 128-key tiles of K and
-// V, the diagonal tile last.  Two CTAs an SM, each with half of tensor memory: while one's
-// softmax runs, the tensor cores have the other's products.
+// V, the diagonal tile last.  A stream of items is 256 threads and half of tensor memory; an SM has two,
+// so that while one's softmax runs the tensor cores have the other's products.  Where a kv head
+// has an even number of query heads, the two are one CTA's and take the two heads of a pair over
+// one ring of K and V tiles: a tile then costs one write into shared memory for two products.
+// Shared memory is the narrowest place at d = 128: S reads 64 KB a tile, PV 32 KB, and the
+// tile itself is 64 KB, 1280 cycles of 128 bytes in all against 1024 of the tensor cores; 1024
+// each where two share it.  Else the streams are CTAs of their own.
 //
 //   warp 0      TMA: the item's Q tile, then K_0 V_0 K_1 V_1 ... through a ring of tiles.
-//   warp 1      one thread issues S = Q K^T (M = 128, N = 128) into tensor memory and O += P V with
-//               P from tensor memory, the first half of P's keys as soon as it is there.
-//               d = 128: S and O fill the CTA's 256 columns, so P takes the place of S and the
+//   warp 1      issues S = Q K^T (M = 128, N = 128) into tensor memory and O += P V with P from tensor
+//               memory, the first half of P's keys as soon as it is there.
+//               d = 128: S and O fill the stream's 256 columns, so P takes the place of S and the
 //               order is PV(j), S(j + 1).  d = 64: P has columns of its own and S(j + 1) is issued
 //               once the scores of S(j) have been read.  S(0) of the next item follows the same way.
 //   warps 2, 3  look over the V tiles that reach past the item's first query (below).
 //   warps 4-7   softmax, one thread a query row, all 128 scores of a tile in registers (the
-//               producers' warpgroup gives up registers for that): no exchange between
-//               threads.  Running maximum moved only when it grows by more than 8 (log2
-//               units), so P <= 2^8 and O is rarely rescaled; fp32 sum of the unrounded weights.
-//               Only the diagonal tile is masked.  At the end O / sum goes to the output row.
+//               other warps give up registers for that): no exchange between threads.
+//               Running maximum moved only when it grows by more than 8 (log2 units), so
+//               P <= 2^8 and O is rarely rescaled; fp32 sum of the unrounded weights.  A diagonal
+//               tile goes block by block, those of 32 keys that none of a warp's queries sees are
+//               passed over.  At the end O / sum goes to the output row.
+//
+// Measured (bf16, one GB300): 8192 and 7500 tokens, 32 heads on 8 kv heads, d = 128: 674 us, 1500
+// TFLOP/s, 0.80 of the measured cuBLAS burst; first version 891 us, with streams as CTAs of their
+// own 789.  64 prompts of 32 to 384, 16 heads, d = 64: 43 us against 16 us of reading and
+// writing once: a softmax warp's item is some 1500 instructions that wait for one another, and
+// tensor memory has room for two such chains an SM; four, with 64-key tiles, took as long.
 //
 // Items are taken longest first: with causal masking the cost of a query tile is its place
 // in its sequence, so the list is by falling place, all sequences long enough and all
@@ -51,28 +63,32 @@ constexpr int kT = 128;                  // queries of an item, keys of a tile
 constexpr int kMaxPrompts = 4096;        // sequences of a call (their bounds are held in shared memory)
 constexpr int kMaxCausalLen = 262144;    // tokens of a sequence (its tile counts are held there too)
 
-template <int D>
+// PAIR: a CTA runs two streams of items side by side, the heads 2 i and 2 i + 1 of one kv head, over one ring
+// of K and V tiles; else one stream, and two CTAs an SM.  A stream has 256 threads and 256 columns of
+// tensor memory either way.
+template <int D, bool PAIR>
 struct Shape {
+  static constexpr int kStreams = PAIR ? 2 : 1;
+  static constexpr int kThreads = 256 * kStreams;          // a stream's warps 0-3: TMA, MMA, V's watch; 4-7: softmax
+  static constexpr uint32_t kTmemCols = 256 * kStreams;
   static constexpr uint32_t kTileBytes = kT * D * 2;
   static constexpr bool kApart = D == 64;                  // P in columns of its own
-  static constexpr int kQ = D == 64 ? 2 : 1;               // Q buffers
-  // Ring of K / V tiles (two CTAs' shared memory in 227 KB).  An even number, so that a slot is K's or
-  // V's for good: who waits for V tiles only must not find a K tile's phase in between.
-  static constexpr int kSlots = D == 64 ? 4 : 2;
+  static constexpr int kQ = D == 64 ? 2 : 1;               // Q buffers of a stream
+  // Ring of K / V tiles.  An even number, so that a slot is K's or V's for good: who waits for V tiles
+  // only must not find a K tile's phase in between.
+  static constexpr int kSlots = D == 64 || PAIR ? 4 : 2;
   static constexpr int kVSlots = kSlots / 2;               // V's, in turn
-  static constexpr uint32_t kColP = kApart ? 192 : 0, kColO = 128;   // S at column 0
-  static constexpr uint32_t kOffRing = kQ * kTileBytes;
+  static constexpr uint32_t kColP = kApart ? 192 : 0, kColO = 128;   // S at column 0 of the stream's
+  static constexpr uint32_t kOffRing = kStreams * kQ * kTileBytes;
   static constexpr uint32_t kOffStage = kOffRing + kSlots * kTileBytes;   // 2 KB a softmax warp: rows on their way out
-  static constexpr uint32_t kOffBar = kOffStage + 4 * 2048;
-  static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
+  static constexpr uint32_t kOffBar = kOffStage + kStreams * 4 * 2048;
+  static constexpr uint32_t kOffMisc = kOffBar + kStreams * 32 * 8;
   static constexpr uint32_t kOffList = kOffMisc + 32;
 };
-constexpr int kThreads = 256;            // warps 0-3: TMA, MMA, V's watch; warps 4-7: softmax
-constexpr uint32_t kTmemCols = 256;
-// Registers: launched with 128 a thread, 32768 a CTA (checked at the first launch: a split above
+// Registers: launched with 128 a thread, 32768 a stream (checked at the first launch: a split above
 // what the launch has would wait for ever); 128 threads keep 80, the softmax's 128 take 176.
 constexpr int kLaunchRegs = 128, kLowRegs = 80, kHighRegs = 176;
-static_assert(128 * (kLowRegs + kHighRegs) == kLaunchRegs * kThreads, "the split must be the launch's registers");
+static_assert(kLowRegs + kHighRegs == 2 * kLaunchRegs, "the split must be the launch's registers");
 
 // The item list: in shared memory the sequences by falling number of items and, for each place i
 // in a sequence, how many items lie at later places.
@@ -228,23 +244,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int D, bool PAIR>
+__global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
     attention_causal_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, int q_x, int k_x, int v_x,
                             const T* __restrict__ v_rows, int kv_stride, const int32_t* __restrict__ cu, int B,
                             int T_max, int max_len, int nh, int group, int classes, T* __restrict__ out,
                             float scale_log2, int32_t* err) {
-  using S = Shape<D>;
+  using S = Shape<D, PAIR>;
   constexpr int HB = D / 64;                       // 64-column boxes of a row
   constexpr uint32_t kBox = kT * 128;              // bytes of one box: 128 rows of 128 bytes
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;
+  const int xs = PAIR ? threadIdx.x >> 8 : 0;      // stream
+  uint8_t* sQ = smem + xs * (S::kQ * S::kTileBytes);
   uint8_t* ring = smem + S::kOffRing;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
-  uint64_t* full = bars;                           // [kSlots] a ring tile has landed
-  uint64_t* empty = bars + 4;                      // [kSlots] its last product is done
+  uint64_t* shared_bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint64_t* bars = shared_bars + 32 * xs;
+  uint64_t* full = shared_bars;                    // [kSlots] a ring tile has landed
+  uint64_t* empty = shared_bars + 4;               // [kSlots] its last product (of each stream) is done
   uint64_t* q_full = bars + 8;                     // [kQ]
   uint64_t* q_empty = bars + 10;                   // [kQ] the item's last S is done
   uint64_t* s_full = bars + 12;                    // S computed (P over S: and every PV before it)
@@ -254,12 +272,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* o_full = bars + 17;                    // the item's last PV is done
   uint64_t* o_free = bars + 18;                    // O read out by the four warps
   uint64_t* drain = bars + 19;
-  uint64_t* v_ready = bars + 20;                   // [kSlots] a V tile has landed and been looked over
+  uint64_t* v_ready = shared_bars + 20;            // [kSlots] a V tile has landed and been looked over
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   int* s_status = reinterpret_cast<int*>(smem + S::kOffMisc + 8);
   volatile int* met = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 12);   // V held an element that is not finite
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_id() & 7, lane = lane_id();   // warp of the stream
 
   pdl_wait();
   pdl_trigger();
@@ -268,9 +286,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     *met = 0;
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], S::kStreams);
       mbar_init(&v_ready[i], 2);
     }
+  }
+  if ((threadIdx.x & 255) == 0) {
     for (int i = 0; i < S::kQ; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
@@ -290,19 +310,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   List list;
   // (the list's scratch words lie where the tiles will be)
-  if (!build_list(cu, B, T_max, max_len, nh, classes, err, s_status, smem + S::kOffList, reinterpret_cast<int*>(smem),
+  if (!build_list(cu, B, T_max, max_len, nh / S::kStreams, classes, err, s_status, smem + S::kOffList, reinterpret_cast<int*>(smem),
                   list))
     return;
   if (item_of_round(0, list.total) < 0) return;    // the whole CTA; nothing allocated yet
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
+  if (threadIdx.x < 32) {
+    tmem_alloc(tmem_slot, S::kTmemCols);
     tmem_relinquish();
   }
   fence_proxy_async_smem();   // the list's scratch words come before the tiles that TMA writes there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem0 = *tmem_slot, tmem = tmem0 + 256u * xs;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
@@ -325,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int r = 0; ok; ++r) {
           const int g = item_of_round(r, list.total);
           if (g < 0) break;
-          const CausalItem it = walk.at(g);
+          CausalItem it = walk.at(g);
+          it.h = it.h * S::kStreams + xs;
           const int kv_col = it.h / group * D;
           const int n = it.tiles();
           const uint32_t b = nq % S::kQ;
@@ -338,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int c = 0; c < HB; ++c)
             tma_load_2d(sQ + b * S::kTileBytes + c * kBox, &tq, &q_full[b], q_x + it.h * D + 64 * c, it.c0 + it.q0);
           ++nq;
+          if (xs) continue;                            // the ring is stream 0's to fill
           for (int j = 0; j < n && ok; ++j)
             ok = load(&tk, k_x + kv_col, it.c0 + j * kT) && load(&tv, v_x + kv_col, it.c0 + j * kT);
         }
@@ -460,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         mbar_wait_bounded(drain, 0, nullptr);
       }
-    } else {
+    } else if (xs == 0) {
       // ------------------------------------------------------------ V: what some queries must not see
       // Every V tile passes here on its way to the product.  In a tile that reaches past the
       // item's first query, rows past the sequence become zero, and elements that are not finite
@@ -527,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t t_p = t_s + S::kColP, t_o = t_s + S::kColO;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
-    uint8_t* stage = smem + S::kOffStage + quad * 2048;
+    uint8_t* stage = smem + S::kOffStage + (4 * xs + quad) * 2048;
     uint32_t ns = 0, no = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -536,7 +558,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     Walk walk(list);
     int g = item_of_round(0, list.total);            // >= 0 here
-    CausalItem it = walk.at(g), nx = it;
+    auto item = [&](int i) {
+      CausalItem t = walk.at(i);
+      t.h = t.h * S::kStreams + xs;
+      return t;
+    };
+    CausalItem it = item(g), nx = it;
     for (int r = 1; g >= 0; ++r, it = nx) {
       const int nt = it.tiles();
       const bool live = it.q0 + quad * 32 < it.len;   // some of this warp's queries exist
@@ -696,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         ++ns;
       }
       g = item_of_round(r, list.total);
-      if (g >= 0) nx = walk.at(g);                   // while the last PV runs
+      if (g >= 0) nx = item(g);                      // while the last PV runs
       if (!ok || !wait(o_full, no & 1u)) {
         ok = false;
         break;
@@ -762,10 +789,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (threadIdx.x < 32) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem0, S::kTmemCols);
   }
 }
 
@@ -775,27 +802,34 @@ struct Maps {
   int q_x = 0, k_x = 0, v_x = 0;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool PAIR>
 cudaError_t launch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
-  using S = Shape<D>;
+  using S = Shape<D, PAIR>;
   const int classes = (a.max_len + kT - 1) / kT;
   const size_t smem = 1024 + S::kOffList + list_bytes(a.B, classes);
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(
-      attention_causal_kernel<T, D>, 1024 + S::kOffList + list_bytes(kMaxPrompts, kMaxCausalLen / kT), kLaunchRegs);
+  const cudaError_t e =
+      limit.raise(attention_causal_kernel<T, D, PAIR>,
+                  1024 + S::kOffList + list_bytes(kMaxPrompts, kMaxCausalLen / kT), kLaunchRegs);
   if (e != cudaSuccess) return e;
   // never more CTAs than items: ceil(len / 128) <= len / 128 + 1 for each sequence
-  const long long most = (static_cast<long long>(a.T_max) / kT + a.B) * a.nh;
-  const long long room = 2LL * num_sms();
+  const long long most = (static_cast<long long>(a.T_max) / kT + a.B) * (a.nh / S::kStreams);
+  const long long room = (PAIR ? 1LL : 2LL) * num_sms();
   const int grid = static_cast<int>(most < room ? most : room);
-  return launch_pdl(attention_causal_kernel<T, D>, dim3(grid), dim3(kThreads), smem, stream, t.q, t.k, t.v, t.q_x,
-                    t.k_x, t.v_x, static_cast<const T*>(a.v), a.kv_stride, a.cu, a.B, a.T_max, a.max_len, a.nh,
+  return launch_pdl(attention_causal_kernel<T, D, PAIR>, dim3(grid), dim3(S::kThreads), smem, stream, t.q, t.k, t.v,
+                    t.q_x, t.k_x, t.v_x, static_cast<const T*>(a.v), a.kv_stride, a.cu, a.B, a.T_max, a.max_len, a.nh,
                     a.nh / a.nkv, classes, static_cast<T*>(a.out), a.scale * 1.4426950408889634f, a.err);
 }
 
 template <typename T>
 cudaError_t dispatch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
-  return a.d == 64 ? launch<T, 64>(t, a, stream) : launch<T, 128>(t, a, stream);
+  // Pairs of heads wherever a kv head has an even number of them.  Pairs against single streams, 32 heads on
+  // 8 kv heads, d = 128: 674 / 789 us for two prompts of 8192 and 7500, 286 / 317 us for 32 of 1024, 132 / 129
+  // us for 256 of 128, 192 / 219 us for 512 of 64; 16 heads on 4, d = 64: 340 / 357 us for 8 of 4096,
+  // 61 / 61 us for 256 of 128.
+  const bool pair = (a.nh / a.nkv) % 2 == 0;
+  if (a.d == 64) return pair ? launch<T, 64, true>(t, a, stream) : launch<T, 64, false>(t, a, stream);
+  return pair ? launch<T, 128, true>(t, a, stream) : launch<T, 128, false>(t, a, stream);
 }
 
 }  // namespace
