@@ -849,18 +849,18 @@ cudaError_t launch_attention_causal(const CausalArgs& a, cudaStream_t stream) {
   const uintptr_t first = std::min(q, std::min(k, v));
   const uintptr_t end = std::max(q + 2u * static_cast<uintptr_t>(a.nh) * a.d,
                                  std::max(k, v) + 2u * static_cast<uintptr_t>(a.nkv) * a.d);
-  auto map = [&](CUtensorMap* m, const void* base, int cols, int stride) {
-    return make_tmap_2d(m, base, dt, 2, a.T_max, cols, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B, stride);
+  // A map's row is a whole stride, whatever part of it is this tensor's: the boxes that are loaded
+  // lie inside the heads' columns.
+  auto map = [&](CUtensorMap* m, const void* base, int stride) {
+    return make_tmap_2d(m, base, dt, 2, a.T_max, stride, kT, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   if (a.q_stride == a.kv_stride && end - first <= 2u * static_cast<uintptr_t>(a.q_stride)) {
-    if (!map(&t.q, reinterpret_cast<const void*>(first), static_cast<int>((end - first) / 2), a.q_stride))
-      return cudaErrorInvalidValue;
+    if (!map(&t.q, reinterpret_cast<const void*>(first), a.q_stride)) return cudaErrorInvalidValue;
     t.k = t.v = t.q;
     t.q_x = static_cast<int>((q - first) / 2);
     t.k_x = static_cast<int>((k - first) / 2);
     t.v_x = static_cast<int>((v - first) / 2);
-  } else if (!map(&t.q, a.q, a.nh * a.d, a.q_stride) || !map(&t.k, a.k, a.nkv * a.d, a.kv_stride) ||
-             !map(&t.v, a.v, a.nkv * a.d, a.kv_stride)) {
+  } else if (!map(&t.q, a.q, a.q_stride) || !map(&t.k, a.k, a.kv_stride) || !map(&t.v, a.v, a.kv_stride)) {
     return cudaErrorInvalidValue;
   }
   return a.dtype == RPP_F16 ? dispatch<__half>(t, a, stream) : dispatch<__nv_bfloat16>(t, a, stream);

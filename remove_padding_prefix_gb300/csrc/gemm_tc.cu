@@ -89,11 +89,11 @@ EncodeTiledFn get_encode_fn() {
 }  // namespace
 
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, long long rows,
-                  int cols, int box_rows, int box_cols, CUtensorMapSwizzle swz, int row_stride) {
+                  int cols, int box_rows, int box_cols, CUtensorMapSwizzle swz) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride ? row_stride : cols) * elem_bytes};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem_bytes};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,

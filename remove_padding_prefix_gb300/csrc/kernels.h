@@ -156,10 +156,9 @@ void set_gemm_stall_next(unsigned long long limit_ns);
 cudaError_t launch_gemm_f32(const float* a, const float* w_t, const float* bias, const float* residual, float* out,
                             int M_max, const int32_t* rows, int N, int K, int epi, int32_t* err, cudaStream_t stream);
 
-// 2D row-major [rows, cols] tensor map, box = box_cols x box_rows, rows row_stride elements
-// apart (0: cols) (defined with the GEMM)
+// 2D row-major [rows, cols] tensor map, box = box_cols x box_rows (defined with the GEMM)
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, long long rows,
-                  int cols, int box_rows, int box_cols, CUtensorMapSwizzle swz, int row_stride = 0);
+                  int cols, int box_rows, int box_cols, CUtensorMapSwizzle swz);
 // persistent longest-first tcgen05 varlen attention (S, P, O in tensor memory), head size 64
 bool attention_sched_supported(int B, int max_len);
 // i8_scales: device (s_q, s_k, s_v) for int8 codes held in bf16 (dtype RPP_BF16, fp16 out);

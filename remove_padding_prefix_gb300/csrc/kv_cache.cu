@@ -585,10 +585,12 @@ cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* fro
   const cudaError_t e = launch_pdl(kv_reserve_kernel<true>, dim3(1), dim3(kPlanThreads), smem, stream, d, c.table,
                                    c.lens, c.refs, to, from, n, err);
   if (e != cudaSuccess) return e;
-  // eight CTAs an SM over all pairs, each thread with at least one round of four vectors
+  // More CTAs than fit at once: the pairs' last pages are full to different degrees, and a share of
+  // an empty one costs a CTA's start only.  16 prompts forked 8 times over 12 layers, with the free
+  // before it: 71 us at 8 CTAs an SM, 64 at 32, 71 at 64, 87 at 128.
   const long long vec = static_cast<long long>(d.layers) * 2 * d.kv_heads * (d.page_size - 1) * (d.head_dim / 8);
-  const int x = blocks_for(n, 8 * num_sms());
-  const int y = blocks_for(vec / (4 * kMoveThreads) + 1, (8 * num_sms() + x - 1) / x);
+  const int x = blocks_for(n, 32 * num_sms());
+  const int y = blocks_for(vec / (4 * kMoveThreads) + 1, (32 * num_sms() + x - 1) / x);
   return launch_pdl(kv_fork_copy_kernel, dim3(x, y), dim3(kMoveThreads), 0, stream, d, static_cast<uint4*>(c.pool),
                     c.table, static_cast<const int32_t*>(c.lens), c.refs, from, to, n, err);
 }
