@@ -467,7 +467,7 @@ RPP_API rpp_status rpp_patch_merge_forward(const rpp_merge_cfg* cfg, const void*
  * never read.  Free pages are taken lowest number first, in the order of the call's list:
  * the state after a call depends on the state before it and nothing else.
  *
- * Lists of slots are device int32[n], n <= 4096.  `err` is required by the calls that change
+ * Lists of slots are device int32[n], 1 <= n <= 4096.  `err` is required by the calls that change
  * a cache.  A slot out of range, or given twice to reserve, append, fork (destinations) or free,
  * records RPP_DERR_SLOT and changes nothing.  reserve and fork change nothing on any error;
  * the others skip the sequence (or row) whose length or page is wrong, record
@@ -508,8 +508,8 @@ RPP_API rpp_status rpp_kv_reserve(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  *              slots[i], in order; NULL: one row each (rows_max >= n).  Rows from cu[n] on
  *              are not read.
  * The rows go to positions lens - count .. lens - 1, reserved before (once for all layers).
- * RPP_DERR_LENGTH: more rows than the sequence has tokens; RPP_DERR_PAGE: a page that is
- * shared with another sequence; RPP_DERR_ROWS: cu[n] > rows_max. */
+ * RPP_DERR_LENGTH: more rows than the sequence has tokens, or a row before cu[0]; RPP_DERR_PAGE:
+ * a page that is shared with another sequence; RPP_DERR_ROWS: cu[n] > rows_max. */
 RPP_API rpp_status rpp_kv_append(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* k,
                                  const void* v, int row_stride, const int32_t* slots, const int32_t* cu_seqlens, int n,
                                  int rows_max, int32_t* err, rpp_stream stream);
@@ -547,7 +547,7 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
  *          QKV projection's output); T_max rows each
  *  out     device [T_max, nh * d] of dtype; rows >= cu[B] untouched; may alias none of q, k, v
- * d 64 or 128; dtype RPP_F16 or RPP_BF16; nh % nkv == 0; B <= 4096; every length <= max_len <=
+ * d 64 or 128; dtype RPP_F16 or RPP_BF16; nh % nkv == 0; scale > 0 and finite; B <= 4096; every length <= max_len <=
  * 262144 (RPP_DERR_LENGTH; RPP_DERR_ROWS if cu[B] > T_max). */
 RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, const void* v, int q_stride,
                                                int kv_stride, const int32_t* cu_seqlens, int B, int T_max,
@@ -560,10 +560,12 @@ RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, con
  * (reserve, append) before the call; a sequence of length 0 gives zeros.
  *  q      device rows of nh * head_dim of dtype, q_stride elements apart (a multiple of 8)
  *  slots  device int32[n], NULL: slots 0 .. n-1; a slot may be named several times
- *  out    device [n, nh * head_dim] of dtype
+ *  out    device [n, nh * head_dim] of dtype; must not overlap q.  After a device error
+ *         (RPP_DERR_SLOT, _LENGTH, _PAGE) its contents are unspecified
  *  workspace  device, 256-byte aligned, >= rpp_attention_decode_workspace_bytes(cfg, n, nh)
  *             bytes, needs no initial contents; not shared by calls that may overlap
- * head_dim 64 or 128, page_size % 16 == 0 (RPP_EUNSUPPORTED otherwise), nh % kv_heads == 0. */
+ * head_dim 64 or 128, page_size % 16 == 0 (RPP_EUNSUPPORTED otherwise), nh % kv_heads == 0,
+ * n <= 4096, scale > 0 and finite. */
 RPP_API size_t rpp_attention_decode_workspace_bytes(const rpp_kv_cfg* cfg, int n, int nh);
 RPP_API rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* q,
                                         int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,

@@ -395,7 +395,8 @@ def _rows(name, t, width, dtype) -> int:
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[1] != width or stride[1] != 1 or t.dtype is not dtype:
         raise ValueError(f"{name}: expected rows of {width} contiguous {dtype}")
-    return stride[0] if shape[0] > 1 else max(stride[0], width)
+    # the stride of a single row is whatever made the view: any valid one will do
+    return stride[0] if shape[0] > 1 or (stride[0] >= width and stride[0] % 8 == 0) else width
 
 
 class KvCache:

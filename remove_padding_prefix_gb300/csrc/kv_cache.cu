@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kMoveThreads)
           else hi = mid - 1;
         }
         i = lo;
-        back = static_cast<long long>(cu[i + 1]) - t;
+        back = t < cu[i] ? 0 : static_cast<long long>(cu[i + 1]) - t;   // rows before cu[0] are nobody's
       }
       const int s = slots[i];
       const int len = lens[s];

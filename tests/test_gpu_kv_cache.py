@@ -298,3 +298,83 @@ def test_a_captured_step_replays():
         p.ref.reserve(sl, ct)
         p.ref.append(0, kw, vw, sl, ct)
         p.check()
+
+
+def test_rows_before_the_first_sequence():
+    p = _some()
+    k, v, _, _ = p.rows(4)
+    before = p.gpu.pool.clone()
+    rpp.kv_append(p.gpu, 0, k[:2], v[:2], ints([0]), ints([2, 2]))   # two rows that are nobody's
+    assert rpp.get_device_error(p.gpu.err) == od.LENGTH
+    assert torch.equal(words_t(p.gpu.pool), words_t(before))
+
+
+def test_one_page():
+    p = Pair(1, 1, 16, 1, 64, 2, 1)
+    p.compact()
+    p.grow([1], [16])
+    p.compact()
+    p.check()
+    rpp.kv_reserve(p.gpu, ints([0]), ints([1]))
+    p.check(od.FULL)
+    p.free([1])
+    p.compact(apart=True)
+    p.check()
+
+
+def test_the_longest_lists():
+    n = 4096
+    p = Pair(1, 9000, 4, 1, 8, 2 * n, 3)
+    r = np.random.default_rng(1)
+    slots = [int(x) for x in r.permutation(2 * n)[:n]]
+    p.grow(slots, [int(x) for x in r.integers(0, 7, n)])
+    p.check()
+    rest = [s for s in range(2 * n) if p.ref.lens[s] == 0][:n]
+    held = [s for s in slots if p.ref.lens[s]]
+    p.fork([held[int(x)] for x in r.integers(0, len(held), n)], rest)
+    p.check()
+    p.free(slots)
+    p.check()
+    p.compact()
+    p.check()
+
+
+def test_offsets_past_32_bits():
+    """A pool of over 2^32 elements, the low pages taken: everything happens behind them."""
+    pages, nkv, d, ps = 150000, 8, 128, 16
+    c = rpp.KvCache(1, pages, ps, nkv, d, 6, 40, "bf16", dev())
+    assert c.pool.numel() > 1 << 32
+    held = 140000
+    c.refs[:held] = 1
+    g = torch.Generator(device=dev()).manual_seed(0)
+    rpp.kv_reserve(c, ints([1, 4]), ints([600, 9]))
+    x = torch.randn(609, 2 * nkv * d, generator=g, device=dev()).bfloat16()
+    rpp.kv_append(c, 0, x[:, :nkv * d], x[:, nkv * d:], ints([1, 4]), ints([0, 600, 609]))
+    rpp.kv_fork(c, ints([1]), ints([0]))
+
+    def rows(slot, n):
+        t = c.table[slot, :-(-n // ps)].long()
+        return c.pool[0, t].permute(1, 0, 3, 2, 4).reshape(2, -1, nkv * d)[:, :n]
+
+    def same():
+        for slot, at, n in ((1, 0, 600), (4, 600, 9), (0, 0, 600)):
+            assert torch.equal(rows(slot, n)[0], x[at:at + n, :nkv * d])
+            assert torch.equal(rows(slot, n)[1], x[at:at + n, nkv * d:])
+
+    assert int(c.table[1, 0]) == held and int(c.table[0].max()) >= held
+    same()
+    q = torch.randn(3, 16 * d, generator=g, device=dev()).bfloat16()
+    out = rpp.attention_decode(c, 0, q, ints([1, 4, 0]))
+    for i, (at, n) in enumerate(((0, 600), (600, 9), (0, 600))):
+        K, V = (y.double().view(n, nkv, d) for y in (x[at:at + n, :nkv * d], x[at:at + n, nkv * d:]))
+        z = torch.einsum("hgd,nhd->hgn", q[i].double().view(nkv, 2, d), K) * d ** -0.5
+        ref = torch.einsum("hgn,nhd->hgd", torch.softmax(z, -1), V).flatten()
+        # a rounding of the output, and 2^-10 of the largest value for the rest (test_gpu_decode.py derives less)
+        assert ((out[i].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * V.abs().max()).all()
+    rpp.kv_free(c, ints([4]))
+    c.refs[100:200] = 0                              # holes far below
+    rpp.kv_compact(c)
+    assert rpp.get_device_error(c.err) == 0
+    assert int(c.table[1].max()) < held and int(c.table[1, :38].min()) >= 0
+    for slot in (1, 0):
+        assert torch.equal(rows(slot, 600)[0], x[:600, :nkv * d]) and torch.equal(rows(slot, 600)[1], x[:600, nkv * d:])

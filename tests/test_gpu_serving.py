@@ -1,6 +1,10 @@
 """The decoder calls as a serving loop uses them: prompts attend and fill the cache, steps reserve, append and attend,
 beams fork, finished sequences leave, the cache is compacted under way.  Every output against fp64 over each
 sequence's own history, kept apart from the cache."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -153,3 +157,41 @@ def test_a_captured_step():
             r.took(order, layer, k, v)
             r.check(outs[layer], q, order, layer)
     r.done()
+
+
+FIRST = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import remove_padding_prefix_gb300 as rpp
+ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+c = rpp.KvCache(1, 40, 16, 2, {d}, 4, 8)
+qkv = torch.randn(50, 8 * {d}, device="cuda").bfloat16()
+w = {d}
+q, k, v = qkv[:, :4 * w], qkv[:, 4 * w:6 * w], qkv[:, 6 * w:]
+slots, lens, cu, src, dst, one = ints([0, 1]), ints([20, 30]), ints([0, 20, 50]), ints([0]), ints([2]), ints([1])
+ws = rpp.attention_decode_workspace(c, 2, 4)
+last = q[[19, 49]]
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    rpp.kv_reserve(c, slots, lens)
+    rpp.kv_append(c, 0, k, v, slots, cu)
+    a = rpp.attention_causal_varlen(q, k, v, cu, 2, 50, 4, 2, w, err=c.err)
+    b = rpp.attention_decode(c, 0, last, slots, workspace=ws)
+    rpp.kv_fork(c, src, dst)
+    rpp.kv_free(c, one)
+    table, refs, live = rpp.kv_compact(c)
+g.replay()
+assert rpp.get_device_error(c.err) == 0
+assert (a[[19, 49]].float() - b.float()).abs().max() <= 2.0 ** -6 * a.float().abs().max()
+assert live.tolist() == [3] and c.lens.tolist() == [20, 0, 20, 0]
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_first_calls_of_a_process_captured(d):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, d=d)], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
