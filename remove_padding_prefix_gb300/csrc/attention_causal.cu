@@ -740,18 +740,6 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
       const float inv = __fdividef(1.0f, l);
-      // Elements that were taken out of the diagonal tile are added back from memory to the rows
-      // that see them.  (The note is visible here: o_full came after the v_ready of that tile.)
-      if (*met != 0 && it.q0 + row < it.len) {
-        for (int k = it.q0; k <= it.q0 + row; ++k) {
-          const T* vr = v_rows + static_cast<long long>(it.c0 + k) * kv_stride + it.h / group * D;
-#pragma unroll
-          for (int e = 0; e < D; ++e) {
-            const float f = to_f32(vr[e]);
-            if (!isfinite(f)) ov[e] = __float_as_uint(__uint_as_float(ov[e]) + f);
-          }
-        }
-      }
       // A thread has a row, a store wants whole lines: 32 columns at a time through 2 KB of shared
       // memory of the warp's own (16-byte chunk u of row r at u ^ (r / 2 & 3): no bank conflict
       // either way), then four lanes a row.
@@ -779,6 +767,21 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
           if (8 * u < rows_left) *reinterpret_cast<uint4*>(obase + 8 * u * pitch + 32 * c) = w;
         }
         __syncwarp();
+      }
+      // Elements that were taken out of the diagonal tile are added back, from memory, to the rows that
+      // see them: such an output is not finite either, so nothing is lost in adding it to the rounded
+      // one.  (The note is visible here: o_full came after the v_ready of that tile.)
+      if (*met != 0 && it.q0 + row < it.len) {
+        T* mine = out + (it.c0 + it.q0 + row) * pitch + it.h * D;   // stored by this warp, before a __syncwarp
+#pragma unroll 1
+        for (int k = it.q0; k <= it.q0 + row; ++k) {
+          const T* vr = v_rows + static_cast<long long>(it.c0 + k) * kv_stride + it.h / group * D;
+#pragma unroll 1
+          for (int e = 0; e < D; ++e) {
+            const float f = to_f32(vr[e]);
+            if (!isfinite(f)) mine[e] = from_f32<T>(to_f32(mine[e]) + f);
+          }
+        }
       }
     }
     if (!ok && lane == 0) {
