@@ -22,7 +22,7 @@
 //   warps 4-7   softmax, one thread a query row, all 128 scores of a tile in registers (the
 //               other warps give up registers for that): no exchange between threads.
 //               Running maximum moved only when it grows by more than 8 (log2 units), so
-//               P <= 2^8 and O is rarely rescaled; fp32 sum of the unrounded weights.  A diagonal
+//               P <= 2^8 (fp16: 2^15) and O is rarely rescaled; fp32 sum of the unrounded weights.  A diagonal
 //               tile goes block by block, those of 32 keys that none of a warp's queries sees are
 //               passed over.  At the end O / sum goes to the output row.
 //
@@ -549,6 +549,9 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t t_p = t_s + S::kColP, t_o = t_s + S::kColO;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
+    // fp16 weights (and so their sum and O) are kept 2^7 times as large, up to 2^15: below the smallest
+    // step of fp16, 2^-24, a weight is lost, and a long sequence has many small ones.
+    constexpr float kUp = std::is_same<T, __half>::value ? 7.f : 0.f;
     uint8_t* stage = smem + S::kOffStage + (4 * xs + quad) * 2048;
     uint32_t ns = 0, no = 0;
     bool ok = true;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
             }
           }
           // scores all -inf so far: weights 0, not 2^(-inf + inf)
-          const float nm = m == neg_inf() ? 0.f : -m;
+          const float nm = m == neg_inf() ? 0.f : kUp - m;
           nm2 = f2_pack(nm, nm);
         };
         auto weights = [&](const uint32_t* sc, uint32_t* p, int n2) {   // 2 n2 scores -> n2 pairs of weights

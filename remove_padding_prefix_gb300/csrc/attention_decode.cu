@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
   constexpr int NT = KB / 8;                     // 8-key tiles of a block
   constexpr int CH = D / 8;                      // 16-byte chunks of a row
   constexpr int KS = D / 16;                     // k16 steps of the scores
+  // fp16 weights (and so their sum and the output, too) are kept 2^7 times as large, up to 2^15: below the
+  // smallest step of fp16, 2^-24, a weight is lost, and a long sequence has many small ones.
+  constexpr float kUp = std::is_same<T, __half>::value ? 7.f : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   long long* s_pre = reinterpret_cast<long long*>(smem + kRingBytes);   // [n + 1]
   __shared__ int s_flag;
@@ -401,8 +404,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
       if (move1) m[1] = mx[1];
     }
     // a row whose scores so far are all -inf keeps m = -inf: its P is 0, not 2^(-inf + inf)
-    const float n0 = m[0] == __int_as_float(0xff800000) ? 0.f : -m[0];
-    const float n1 = m[1] == __int_as_float(0xff800000) ? 0.f : -m[1];
+    const float n0 = m[0] == __int_as_float(0xff800000) ? 0.f : kUp - m[0];
+    const float n1 = m[1] == __int_as_float(0xff800000) ? 0.f : kUp - m[1];
     uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {

@@ -139,6 +139,48 @@ def test_scores_far_apart(d, lens):
     assert rpp.get_device_error(err) == 0
     check_rows(out, q, k, v, cu_of(lens), 2, 1, d)
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh", [1, 2])
+def test_many_weights_far_below_the_maximum(d, nh):
+    """65536 fp16 keys, the first 26 powers of two above the others in weight: in the last rows those are
+    2^-10 of the sum, and the output is theirs (the first value is 0, theirs 1).
+
+    Tolerance: two roundings, of the weights and of the output, 2^-11 each; weights of up to 2^8 are
+    kept 2^7 times as large, so what is below fp16's smallest step, 2^-24, is half a step of 2^-7
+    of it off: i 2^-32 in row i; fp32 sums of i like terms, i 2^-24 of each of numerator and denominator;
+    2^-16 for the exponent, 26 2^-23 off; half a step of the smallest fp16 outputs."""
+    n = 65536
+    q, k, v = (torch.zeros(n, w * d, device=dev(), dtype=torch.float16) for w in (nh, 1, 1))
+    q[:, ::d] = 8.0
+    k[0, 0] = 18.02                                                 # score 8 * 18.02 / 8, e^-18.02 = 2^-26
+    v[1:] = 1
+    err = rpp.new_error_word()
+    got = rpp.attention_causal_varlen(q, k, v, ints([0, n]), 1, n, nh, 1, d, scale=0.125, err=err).double()
+    assert rpp.get_device_error(err) == 0
+    i = torch.arange(n, device=dev(), dtype=torch.float64)[:, None]
+    w = torch.exp(-k[0, 0].double()) * i
+    ref = w / (1 + w)
+    limit = ref * (2 * 2.0 ** -11 + 2 * i * 2.0 ** -24 + 2.0 ** -16) + i * 2.0 ** -32 + 2.0 ** -25
+    worst = ((got - ref).abs() - limit).argmax().item() // got.shape[1]
+    assert ((got - ref).abs() <= limit).all(), (worst, float(got[worst, 0]), float(ref[worst]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh", [1, 2])
+def test_weights_as_large_as_the_lazy_maximum_lets_them_be(d, nh):
+    """fp16 scores whose maximum climbs by 7.9 powers of two after the first tile, too little to move it."""
+    lens = [700, 130]
+    q, k, v = make(lens, nh, 1, d, "fp16")
+    q.zero_()
+    q[:, ::d] = 8.0
+    k.zero_()
+    for a, n in ((0, 700), (700, 130)):
+        k[a + 128:a + n, 0] = 5.475                                 # e^5.475 = 2^7.9
+    cu = cu_of(lens)
+    out = rpp.attention_causal_varlen(q, k, v, ints(cu), 2, 700, nh, 1, d, scale=0.125)
+    check_rows(out, q, k, v, cu, nh, 1, d, 0.125)
+
+
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("lens,where", [([300, 200], [5, 127, 128, 130, 255, 256, 299]), ([100, 28], [0, 50, 99]),

@@ -162,6 +162,31 @@ def test_uneven_scores():
     check(rpp.attention_decode(c, 0, q), q, c, 0, [0, 1], 4)
 
 
+def test_many_weights_far_below_the_maximum():
+    """65536 fp16 keys, the first 26 powers of two above the others in weight: together those are
+    2^-10 of the sum, and the output is theirs (the first value is 0, theirs 1).  Queries enough that
+    a warp has a sequence whole.
+
+    Tolerance: the output's rounding, 2^-11 of it; weights of up to 2^8 are kept 2^7 times as large,
+    so what is below fp16's smallest step, 2^-24, is half a step of 2^-7 of it off: n 2^-32; fp32
+    sums of n like terms, n 2^-24 of each of numerator and denominator; 2^-16 for the exponent, 26 2^-23 off."""
+    n, rows = 65536, 2048
+    c = make("fp16", [n], 1, 64, 64, nan=False)
+    c.pool[0, :, 0] = 0
+    c.pool[0, :, 1] = 1
+    first = int(c.table[0, 0])
+    c.pool[0, first, 0, 0, 0, 0] = 18.02                            # score 8 * 18.02 / 8, e^-18.02 = 2^-26
+    c.pool[0, first, 1, 0, 0] = 0
+    q = torch.zeros(rows, 64, device=dev(), dtype=torch.float16)
+    q[:, 0] = 8.0
+    got = rpp.attention_decode(c, 0, q, torch.zeros(rows, dtype=torch.int32, device=dev())).double()
+    assert rpp.get_device_error(c.err) == 0
+    w = torch.exp(-c.pool[0, first, 0, 0, 0, 0].double()) * (n - 1)
+    ref = w / (1 + w)
+    limit = ref * (2.0 ** -11 + 2 * n * 2.0 ** -24 + 2.0 ** -16) + n * 2.0 ** -32
+    assert ((got - ref).abs() <= limit).all(), (float(got.min()), float(got.max()), float(ref))
+
+
 def test_infinite_scores():
     """-inf scores drop their keys; all of them -inf, or a +inf one, give NaN as the formula does."""
     c = make("bf16", [40, 40, 40], 1, 64, 16, nan=False)
