@@ -477,12 +477,12 @@ RPP_API rpp_status rpp_patch_merge_forward(const rpp_merge_cfg* cfg, const void*
  * ------------------------------------------------------------------------------ */
 typedef struct rpp_kv_cfg {
   int layers;
-  int pages;      /* pages of the pool (in each layer) */
-  int page_size;  /* tokens a page; rpp_attention_decode needs a multiple of 16 */
+  int pages;      /* pages of the pool (in each layer); <= 2^30, and the pool below 2^62 bytes */
+  int page_size;  /* tokens a page, <= 65536; rpp_attention_decode needs a multiple of 16 */
   int kv_heads;   /* kv_heads * head_dim <= 65536 */
   int head_dim;   /* multiple of 8; rpp_attention_decode takes 64 and 128 */
   int slots;      /* sequences; <= 65536, slots * max_pages < 2^31 */
-  int max_pages;  /* pages of one sequence at most */
+  int max_pages;  /* pages of one sequence at most; max_pages * page_size <= 2^31 - 65536 */
   int dtype;      /* RPP_F16 or RPP_BF16 */
 } rpp_kv_cfg;
 
@@ -503,7 +503,7 @@ RPP_API rpp_status rpp_kv_reserve(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
 
 /* Writes the K and V rows of the last tokens of n sequences into one layer.
  *  k, v        device rows of kv_heads * head_dim, row_stride elements apart (a multiple of 8,
- *              so both may be columns of a QKV projection's output); rows_max rows
+ *              so both may be columns of a QKV projection's output); rows_max <= 2^31 - 65536 rows
  *  cu_seqlens  device int32[n+1]: rows cu[i] .. cu[i+1]-1 are the last tokens of slot
  *              slots[i], in order; NULL: one row each (rows_max >= n).  Rows from cu[n] on
  *              are not read.
@@ -545,7 +545,7 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  * it, whatever they hold (infinities and NaN among it).
  *  q       device rows of nh * d of dtype, q_stride elements apart; k, v: rows of nkv * d,
  *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
- *          QKV projection's output); T_max rows each
+ *          QKV projection's output); T_max <= 2^31 - 65536 rows each
  *  out     device [T_max, nh * d] of dtype; rows >= cu[B] untouched; may alias none of q, k, v
  * d 64 or 128; dtype RPP_F16 or RPP_BF16; nh % nkv == 0; scale > 0 and finite; B <= 4096; every length <= max_len <=
  * 262144 (RPP_DERR_LENGTH; RPP_DERR_ROWS if cu[B] > T_max). */

@@ -6,6 +6,11 @@
 namespace rpp {
 namespace {
 
+// Rows of a call and tokens of a sequence: a page (65536 rows at most) more is still an int, so counts of pages
+// and tiles are rounded up without care.  The same for pages and the kernels' strides over them.
+constexpr long long kMostRows = 0x7fffffffLL - 65535;
+constexpr int kMostPages = 1 << 30;
+
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 rpp_status kv_cfg_ok(const rpp_kv_cfg* c) {
@@ -13,12 +18,15 @@ rpp_status kv_cfg_ok(const rpp_kv_cfg* c) {
       c->slots <= 0 || c->max_pages <= 0)
     return RPP_EINVAL;
   if (static_cast<long long>(c->slots) * c->max_pages > 0x7fffffffLL ||
-      static_cast<long long>(c->max_pages) * c->page_size > 0x7fffffffLL)
+      static_cast<long long>(c->max_pages) * c->page_size > kMostRows)
     return RPP_EINVAL;
   if (c->dtype != RPP_F16 && c->dtype != RPP_BF16) return RPP_EUNSUPPORTED;
   if (c->head_dim % 8 || c->slots > kKvMaxSlots || c->layers > 65536 || c->page_size > 65536 ||
-      static_cast<long long>(c->kv_heads) * c->head_dim > 65536)
+      static_cast<long long>(c->kv_heads) * c->head_dim > 65536 || c->pages > kMostPages)
     return RPP_EUNSUPPORTED;
+  // bytes of the pool, below 2^62: a layer's pages are at most 2^30 * 2^34 of them
+  const long long page = 4LL * c->kv_heads * c->head_dim * c->page_size;
+  if (page > (1LL << 62) / c->pages / c->layers) return RPP_EUNSUPPORTED;
   return RPP_OK;
 }
 
@@ -72,6 +80,7 @@ rpp_status rpp_kv_append(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int l
   if (!aligned(k, 16) || !aligned(v, 16) || row_stride % 8 || row_stride < cfg->kv_heads * cfg->head_dim)
     return RPP_EINVAL;
   if (!cu_seqlens && rows_max < n) return RPP_EINVAL;
+  if (rows_max > kMostRows) return RPP_EUNSUPPORTED;
   return status_from_cuda(launch_kv_append(dims(cfg), state(cache), layer, k, v, row_stride, slots, cu_seqlens, n,
                                            rows_max, err, static_cast<cudaStream_t>(stream)));
 }
@@ -148,7 +157,7 @@ rpp_status rpp_attention_causal_varlen(const void* q, const void* k, const void*
   if (!(scale > 0.f) || scale > 3.0e38f) return RPP_EINVAL;
   if (dtype != RPP_F16 && dtype != RPP_BF16) return RPP_EUNSUPPORTED;
   if (!attention_causal_supported(B, max_len, d)) return RPP_EUNSUPPORTED;
-  if ((static_cast<long long>(T_max) / 128 + B) * nh > 0x7fffffffLL ||
+  if (T_max > kMostRows || (static_cast<long long>(T_max) / 128 + B) * nh > 0x7fffffffLL ||
       static_cast<long long>(nh) * d > 0x7fffffffLL)
     return RPP_EUNSUPPORTED;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || q_stride % 8 || kv_stride % 8 ||

@@ -34,6 +34,10 @@ BAD_CFG = [
     (dict(head_dim=0), EINVAL), (dict(slots=0), EINVAL), (dict(max_pages=0), EINVAL),
     (dict(slots=65536, max_pages=65536), EINVAL), (dict(max_pages=1 << 28), EINVAL),
     (dict(dtype=_abi.RPP_F32), EUNSUPPORTED), (dict(dtype=_abi.RPP_I8), EUNSUPPORTED),
+    (dict(slots=1, page_size=3, max_pages=715827882), EINVAL),        # 2^31 - 2 tokens: a page more is past an int
+    (dict(pages=(1 << 30) + 1), EUNSUPPORTED),
+    (dict(pages=1 << 30, layers=1 << 16, page_size=1 << 16, kv_heads=512, head_dim=128), EUNSUPPORTED),   # 2^80 bytes
+    (dict(pages=1 << 30, layers=1 << 16, page_size=16, kv_heads=32, head_dim=128), EUNSUPPORTED),         # 2^64 bytes
     (dict(head_dim=60), EUNSUPPORTED), (dict(slots=65537), EUNSUPPORTED), (dict(kv_heads=1025), EUNSUPPORTED),
 ]
 
@@ -87,6 +91,7 @@ def test_arrays(lib, kw):
     (dict(layer=2), EINVAL, ("append", "decode")), (dict(layer=-1), EINVAL, ("append", "decode")),
     (dict(k=None), EINVAL, ("append",)), (dict(v=258), EINVAL, ("append",)),
     (dict(ld=127), EINVAL, ("append",)), (dict(ld=120), EINVAL, ("append",)),
+    (dict(rows=0x7fffffff), EUNSUPPORTED, ("append",)),
     (dict(rows=0), EINVAL, ("append",)), (dict(cu=None, rows=1), EINVAL, ("append",)),
     (dict(out=None), EINVAL, ("compact", "decode")),
     (dict(ws=None), EINVAL, ("compact", "decode")), (dict(ws=260), EINVAL, ("compact", "decode")),
@@ -128,6 +133,7 @@ def test_sizes(lib):
     (dict(dtype=_abi.RPP_F32), EUNSUPPORTED), (dict(dtype=_abi.RPP_I8), EUNSUPPORTED),
     (dict(d=96, ldq=1024, ld=1024), EUNSUPPORTED), (dict(B=4097), EUNSUPPORTED), (dict(max_len=262145), EUNSUPPORTED),
     (dict(nh=1 << 24, T=1 << 20, ldq=1 << 30), EUNSUPPORTED),
+    (dict(T=0x7fffffff), EUNSUPPORTED),
 ])
 def test_causal_arguments(lib, kw, status):
     g = dict(q=256, k=256, v=256, ldq=256, ld=128, cu=256, B=3, T=100, max_len=60, nh=4, nkv=2, d=64,
