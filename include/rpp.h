@@ -469,9 +469,11 @@ RPP_API rpp_status rpp_patch_merge_forward(const rpp_merge_cfg* cfg, const void*
  *
  * Lists of slots are device int32[n], 1 <= n <= 4096.  `err` is required by the calls that change
  * a cache.  A slot out of range, or given twice to reserve, append, fork (destinations) or free,
- * records RPP_DERR_SLOT and changes nothing.  reserve and fork change nothing on any error;
- * the others skip the sequence (or row) whose length or page is wrong, record
- * RPP_DERR_LENGTH or RPP_DERR_PAGE, and stay in bounds.
+ * records RPP_DERR_SLOT and changes nothing.  reserve changes nothing on any error, fork on any
+ * but RPP_DERR_PAGE (a source whose table names pages outside the pool); the others skip
+ * the sequence (or row) whose length or page is wrong, record RPP_DERR_LENGTH or RPP_DERR_PAGE,
+ * and stay in bounds.  Of what such a fork, append or free has yet to do when the word is set,
+ * for other sequences too, any part may be left out; a compaction is carried out for them.
  * Calls on one cache are ordered by their stream; a cache is not to be changed on one
  * stream while another reads it.
  * ------------------------------------------------------------------------------ */
@@ -528,7 +530,7 @@ RPP_API rpp_status rpp_kv_free(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache,
 /* Moves the pages in use to the front of the pool: with `live` of them, the k-th page in
  * use numbered live or above moves, in all layers, to the k-th free page below it.
  *  table_out  device int32[slots, max_pages], refs_out int32[pages]: the cache's table and
- *             counts afterwards (they may be the cache's own arrays; if they are not, the
+ *             counts afterwards (both may be the cache's own arrays; if neither is, the
  *             old ones still describe the old places, whose rows stay until taken again)
  *  remap      device int32[pages] out: each page's new number, -1 for a free one
  *  live       device int32[1] out: pages in use

@@ -115,6 +115,7 @@ rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int3
   const rpp_status st = kv_ok(cfg, cache);
   if (st != RPP_OK) return st;
   if (!table_out || !refs_out || !remap || !live || !workspace || !err) return RPP_EINVAL;
+  if ((table_out == cache->table) != (refs_out == cache->refs)) return RPP_EINVAL;   // the cache's two would part
   if (!aligned(workspace, 8)) return RPP_EINVAL;
   if (workspace_bytes < compact_bytes(cfg)) return RPP_EWORKSPACE;
   return status_from_cuda(launch_kv_compact(dims(cfg), state(cache), table_out, refs_out, remap, live,

@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 // ---------------------------------------------------------------- compact
 // With `live` pages in use, the k-th page in use at or above `live` moves to the k-th free
-// page below it.  moves[0] = their number, moves[1] = live, then (to, from) pairs; remap[p] = the page's new
-// number (-1: not in use).
+// page below it.  moves[0] = their number (-1: the error word was set), moves[1] = live, then (to, from)
+// pairs; remap[p] = the page's new number (-1: not in use).
 __global__ void __launch_bounds__(kPlanThreads)
     kv_compact_plan_kernel(int pages, const int32_t* __restrict__ refs, int32_t* __restrict__ remap,
                            int32_t* __restrict__ live_out, int32_t* __restrict__ moves, const int32_t* err) {
@@ -435,7 +435,10 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_warp[kPlanWarps];
   pdl_wait();
   pdl_trigger();
-  if (quit(err, &s_flag)) return;
+  if (quit(err, &s_flag)) {
+    if (threadIdx.x == 0) moves[0] = -1;
+    return;
+  }
   const int warp = warp_id(), lane = lane_id();
   const int2 st = warp_stretch(pages);
   int mine = 0;
@@ -507,13 +510,14 @@ __global__ void __launch_bounds__(kMoveThreads)
                            const int32_t* __restrict__ lens, const int32_t* refs, int32_t* table_out,
                            int32_t* refs_out, const int32_t* __restrict__ remap, const int32_t* __restrict__ moves,
                            int32_t* err) {
-  __shared__ int s_flag;
   pdl_wait();
   pdl_trigger();
-  if (quit(err, &s_flag)) return;
+  // The plan's word, not the error word: this launch's own CTAs may set that, for a corrupt table, and
+  // the pages of the other sequences have to move all the same, as the table says they did.
+  const int n_moves = moves[0];
+  if (n_moves < 0) return;
   const long long tid = static_cast<long long>(blockIdx.x) * kMoveThreads + threadIdx.x;
   const long long threads = static_cast<long long>(gridDim.x) * kMoveThreads;
-  const int n_moves = moves[0];
   const int2* pairs = reinterpret_cast<const int2*>(moves + 2);
   const long long page_vec = 2LL * d.kv_heads * d.page_size * (d.head_dim / 8);
   const long long layer_vec = page_vec * d.pages;

@@ -95,6 +95,7 @@ def test_arrays(lib, kw):
     (dict(rows=0), EINVAL, ("append",)), (dict(cu=None, rows=1), EINVAL, ("append",)),
     (dict(out=None), EINVAL, ("compact", "decode")),
     (dict(ws=None), EINVAL, ("compact", "decode")), (dict(ws=260), EINVAL, ("compact", "decode")),
+    (dict(out=512), EINVAL, ("compact",)),                             # a new table, but the cache's own counts
     (dict(ws_bytes=8), EWORKSPACE, ("compact", "decode")),
     (dict(q=None), EINVAL, ("decode",)), (dict(q=264), EINVAL, ("decode",)), (dict(ldq=255), EINVAL, ("decode",)),
     (dict(ldq=248), EINVAL, ("decode",)), (dict(nh=3), EINVAL, ("decode",)), (dict(nh=0), EINVAL, ("decode",)),

@@ -259,7 +259,7 @@ def test_a_set_error_word_stops_every_call():
     rpp.kv_append(p.gpu, 0, k, v, ints([0]))
     rpp.kv_fork(p.gpu, ints([0]), ints([2]))
     rpp.kv_free(p.gpu, ints([0]))
-    rpp.kv_compact(p.gpu, table_out=table)
+    rpp.kv_compact(p.gpu, table_out=table, refs_out=torch.zeros_like(p.gpu.refs))
     assert (table == 5).all()
     p.check(42)
 
@@ -378,3 +378,32 @@ def test_offsets_past_32_bits():
     assert int(c.table[1].max()) < held and int(c.table[1, :38].min()) >= 0
     for slot in (1, 0):
         assert torch.equal(rows(slot, 600)[0], x[:600, :nkv * d]) and torch.equal(rows(slot, 600)[1], x[:600, nkv * d:])
+
+
+@pytest.mark.parametrize("name", ["table_out", "refs_out"])
+def test_compact_writes_the_caches_own_table_and_counts_or_neither(name):
+    p = _some()
+    own = p.gpu.table if name == "table_out" else p.gpu.refs
+    with pytest.raises(rpp.RppError):
+        rpp.kv_compact(p.gpu, **{name: torch.empty_like(own)})
+    p.check()
+
+
+def test_compact_with_one_corrupt_table_entry_moves_the_others():
+    """One page number outside the pool: the other sequences' rows are where the new table says,
+    whichever CTAs of the move start after the error word is set."""
+    p = Pair(2, 600, 16, 2, 64, 40, 32)
+    order = np.random.default_rng(4).permutation(40)
+    p.grow([int(s) for s in order], [16 * 14 + int(s) % 16 for s in order])
+    p.free([int(s) for s in order[:20]])
+    p.gpu.table[int(order[20]), 0] = 600
+    old = {int(s): p.gpu.table[int(s)].clone() for s in order[21:]}
+    pool = p.gpu.pool.clone()
+    table, refs, live = rpp.kv_compact(p.gpu)
+    assert rpp.get_device_error(p.gpu.err) == od.PAGE
+    n = int(live)
+    for s, row in old.items():
+        used = -(-int(p.gpu.lens[s]) // 16)
+        new = table[s, :used].long()
+        assert (new < n).all() and (new >= 0).all()
+        assert torch.equal(words_t(p.gpu.pool[:, new]), words_t(pool[:, row[:used].long()]))
