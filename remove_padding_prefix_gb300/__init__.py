@@ -384,6 +384,15 @@ def _here(*tensors) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw), a tensor of the stream that the call runs on: memory of the current stream's could
+    be in use by work queued there, or be given out there again while the call's stream still uses it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _ints(name, t, n=None):
     if t.dtype is not torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{name}: expected a contiguous int32 tensor" + (f" of {n}" if n is not None else ""))
@@ -501,7 +510,7 @@ def kv_free(cache: KvCache, slots, err=None, stream=None):
 def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, live=None, err=None, stream=None):
     """Move the pages in use to the front of the pool; returns (table, refs, live).
 
-    Without table_out and refs_out the cache's own arrays are rewritten; with them the old
+    Without table_out and refs_out the cache's own arrays are rewritten; with both the old
     ones stay as they are (KvCache.adopt takes the new).  live: device int32[1]; remap:
     device int32[pages], each page's new number, for tables of the caller's own."""
     err = cache.err if err is None else err
@@ -509,7 +518,7 @@ def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, live=N
     refs = cache.refs if refs_out is None else refs_out
     remap = cache._remap if remap is None else remap
     if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=cache.pool.device)
+        live = _made(stream, torch.empty, 1, dtype=torch.int32, device=cache.pool.device)
     here = _here(cache.pool, table, refs, remap, live, err)
     cfg, lists = cache.cfg, cache._lists
     _check("rpp_kv_compact",
@@ -520,9 +529,9 @@ def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, live=N
     return table, refs, live
 
 
-def _out_like(q, out, rows, width):
+def _out_like(q, out, rows, width, stream):
     if out is None:
-        return torch.empty((rows, width), dtype=q.dtype, device=q.device)
+        return _made(stream, torch.empty, (rows, width), dtype=q.dtype, device=q.device)
     if out.shape != (rows, width) or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out: expected a contiguous tensor like q")
     return out
@@ -537,7 +546,7 @@ def attention_causal_varlen(q, k, v, cu_seqlens, B: int, max_len: int, nh: int, 
     ldq, ld = _rows("q", q, nh * d, dtype), _rows("k", k, nkv * d, dtype)
     if _rows("v", v, nkv * d, dtype) != ld or k.shape[0] != T_max or v.shape[0] != T_max:
         raise ValueError("q, k and v: expected equal row counts, k and v equal strides")
-    o = _out_like(q, out, T_max, nh * d)
+    o = _out_like(q, out, T_max, nh * d, stream)
     _check("rpp_attention_causal_varlen",
            lib().rpp_attention_causal_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ld,
                                              _ints("cu_seqlens", cu_seqlens, B + 1), B, T_max, max_len, nh, nkv, d,
@@ -564,10 +573,10 @@ def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=
     d = cache._d
     n, width = q.shape
     nh = width // d
-    ws = attention_decode_workspace(cache, n, nh) if workspace is None else workspace
+    ws = _made(stream, attention_decode_workspace, cache, n, nh) if workspace is None else workspace
     here = _here(cache.pool, q, slots, out, ws, err)
     ld = _rows("q", q, nh * d, cache._dtype)
-    o = _out_like(q, out, n, nh * d)
+    o = _out_like(q, out, n, nh * d, stream)
     _check("rpp_attention_decode",
            lib().rpp_attention_decode(cache._cfg, cache._cache, layer, q.data_ptr(), ld,
                                       None if slots is None else _ints("slots", slots, n), n, nh,

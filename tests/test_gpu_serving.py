@@ -159,6 +159,40 @@ def test_a_captured_step():
     r.done()
 
 
+def test_what_a_call_makes_belongs_to_its_stream(monkeypatch):
+    """Workspace, output and count of a call on a given stream: the current stream gets that memory neither
+    while the call's stream is busy nor after, and the call gets none that the current stream has just freed."""
+    loop = Loop(1, 20, 16, 4, 2, 64, 4, 8, "bf16")
+    c = loop.cache
+    q, k, v = loop.qkv(3)
+    rpp.kv_reserve(c, ints([0, 1, 2]), ints([1, 1, 1]))
+    rpp.kv_append(c, 0, k, v, ints([0, 1, 2]))
+    cu = ints([0, 3])
+    sizes = [rpp.attention_decode_workspace(c, 3, 4).numel(), q.numel() * 2, q.numel() * 2, 4]
+    torch.cuda.synchronize()
+    made = []
+    make = rpp.attention_decode_workspace
+    monkeypatch.setattr(rpp, "attention_decode_workspace", lambda *a: made.append(make(*a)) or made[-1])
+    freed = [torch.empty(n, dtype=torch.uint8, device=dev()) for n in sizes]
+    before = {t.data_ptr() for t in freed}
+    del freed                                     # what the current stream would be given next
+    side = torch.cuda.Stream()
+    outs = [rpp.attention_decode(c, 0, q, stream=side),
+            rpp.attention_causal_varlen(q, k, v, cu, 1, 3, 4, 2, 64, err=c.err, stream=side),
+            rpp.kv_compact(c, stream=side)[2]]
+    assert len(made) == 1
+    mine = {t.data_ptr() for t in made + outs}
+    assert not mine & before
+    del made[:]
+    after = [torch.empty(sizes[0], dtype=torch.uint8, device=dev()) for _ in range(4)]
+    assert not mine & {t.data_ptr() for t in after}
+    side.synchronize()
+    assert rpp.get_device_error(c.err) == 0 and int(outs[2]) == 3
+    check_rows(outs[1], q, k, v, [0, 3], 4, 2, 64)
+    # a new token's attention over its own key alone is its value
+    assert torch.equal(outs[0].view(3, 2, 2, 64), v.view(3, 2, 1, 64).expand(3, 2, 2, 64))
+
+
 FIRST = """
 import sys
 sys.path.insert(0, {root!r})
