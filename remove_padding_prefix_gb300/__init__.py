@@ -574,6 +574,8 @@ def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=
     n, width = q.shape
     nh = width // d
     ws = _made(stream, attention_decode_workspace, cache, n, nh) if workspace is None else workspace
+    if not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
     here = _here(cache.pool, q, slots, out, ws, err)
     ld = _rows("q", q, nh * d, cache._dtype)
     o = _out_like(q, out, n, nh * d, stream)

@@ -274,3 +274,13 @@ def test_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for c, o in outs:
         check(o, q, c, 0, range(3), 16)
+
+
+def test_a_workspace_of_fewer_bytes_than_it_counts_is_refused():
+    c = make("bf16", [40], 2, 64, 16)
+    q = queries(1, 4, 64, "bf16")
+    n = rpp.attention_decode_workspace(c, 1, 4).numel()
+    with pytest.raises(ValueError):
+        rpp.attention_decode(c, 0, q, workspace=torch.empty(1, dtype=torch.uint8, device=dev()).expand(n))
+    with pytest.raises(rpp.RppError):
+        rpp.attention_decode(c, 0, q, workspace=torch.empty(n - 1, dtype=torch.uint8, device=dev()))
