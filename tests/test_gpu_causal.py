@@ -292,3 +292,23 @@ def test_ragged_batch_many_times(dtype, d):
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
     check_rows(outs[0], q, k, v, cu, nh, nkv, d, seqs=range(13), heads=[0, 13, 31])
+
+
+def test_two_streams_at_once():
+    """Pairs of heads, single streams and both head sizes side by side: CTAs of different calls share an SM and
+    its tensor memory."""
+    cases = [(64, 4, 2, [300, 1, 900, 128]), (64, 3, 3, [700, 40, 1]), (128, 8, 2, [1500, 3]), (128, 5, 5, [260, 800])]
+    jobs = []
+    for i, (d, nh, nkv, lens) in enumerate(cases):
+        jobs.append((make(lens, nh, nkv, d, "bf16", seed=i), cu_of(lens), ints(cu_of(lens)), rpp.new_error_word(),
+                     torch.cuda.Stream(), [], (nh, nkv, d)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (q, k, v), cu, dcu, err, s, got, (nh, nkv, d) in jobs:
+            with torch.cuda.stream(s):
+                got.append(rpp.attention_causal_varlen(q, k, v, dcu, len(cu) - 1, 1500, nh, nkv, d, err=err))
+    torch.cuda.synchronize()
+    for (q, k, v), cu, _, err, _, got, (nh, nkv, d) in jobs:
+        assert rpp.get_device_error(err) == 0
+        check_rows(got[0], q, k, v, cu, nh, nkv, d)
+        assert all(torch.equal(got[0], g) for g in got)
