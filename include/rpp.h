@@ -559,7 +559,8 @@ RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, con
 /* Attention of one new token per sequence over the cache:
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . K[j]) V[j],  j < lens[slots[i]],
  * K and V of kv head h / (nh / kv_heads).  The new token's own K and V are in the cache
- * (reserve, append) before the call; a sequence of length 0 gives zeros.
+ * (reserve, append) before the call; a sequence of length 0 gives zeros.  A value that is not
+ * finite gives what the formula does: a weight is above 0, however small, but for a score of -inf.
  *  q      device rows of nh * head_dim of dtype, q_stride elements apart (a multiple of 8)
  *  slots  device int32[n], NULL: slots 0 .. n-1; a slot may be named several times
  *  out    device [n, nh * head_dim] of dtype; must not overlap q.  After a device error

@@ -50,6 +50,7 @@
 #include <algorithm>
 
 #include "attention_common.cuh"
+#include "nonfinite.cuh"
 
 namespace rpp {
 
@@ -218,14 +219,6 @@ __device__ __forceinline__ int item_of_round(int r, int total) {
   return g < total ? static_cast<int>(g) : -1;
 }
 
-// bits 15 and 31 set where the low / high 16-bit float of the word is not finite (its exponent all
-// ones, so one more carries out of it); other bits arbitrary
-template <typename T>
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
-  constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
-  constexpr uint32_t one = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
-  return (w & e) + one;
-}
 // the word with the elements that are not finite set to zero
 template <typename T>
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {

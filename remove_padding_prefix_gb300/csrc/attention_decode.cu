@@ -27,10 +27,12 @@
 //    else one for each place where the line was cut (many units of few pieces).
 //
 // Rows past the sequence are filled with zeros in shared memory (never read), so pool
-// pages may hold anything there.
+// pages may hold anything there.  Values of the sequence that are not finite: at the end of a unit
+// outputs that came out NaN in a row whose sum is a number are taken from those values again (nonfinite.cuh).
 #include <type_traits>
 
 #include "kernels.h"
+#include "nonfinite.cuh"
 
 namespace rpp {
 
@@ -443,6 +445,46 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
       }
       const int head = cc.unit / p.parts, part = cc.unit - head * p.parts;
       const int have = min(kRows, p.group - part * kRows);
+      // rows whose sum is a number: all their scores are, or -inf
+      bool sound[2], redo = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float nan = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) nan = max3_nan(nan, o[j][2 * e], o[j][2 * e + 1]);
+        sound[e] = g + 8 * e < have && l[e] > 0.f && l[e] < __int_as_float(0x7f800000);
+        redo = redo || (sound[e] && nan != nan);
+      }
+      if (__any_sync(0xffffffffu, redo)) {
+        // The unit's keys in this share once more, V's elements that are not finite into the outputs.  A K row
+        // that is not finite has the score -inf in a sound row: weight 0, and 0 * inf is NaN.
+        const int here = static_cast<int>(f - f0 < cc.blk ? f - f0 : cc.blk) + 1;
+        const int k1 = min(cc.len, (cc.blk + 1) * KB);
+        uint32_t got = 0;           // columns that have one
+#pragma unroll 1
+        for (int key = (cc.blk + 1 - here) * KB; key < k1; ++key) {
+          const int pg = __ldg(cc.row + key / ps);
+          if (pg < 0 || pg >= p.d.pages) continue;
+          const T* kr = pool + pg * page_elems + head * head_elems + static_cast<long long>(key % ps) * D;
+          const T* vr = kr + v_off;
+          if (!__any_sync(0xffffffffu, part_nonfinite<T, D>(vr + lane * (D / 32)))) continue;
+          const bool none = __any_sync(0xffffffffu, part_nonfinite<T, D>(kr + lane * (D / 32)));
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(vr + 8 * j + 2 * t);
+            const uint32_t bad = nonfinite2<T>(w);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (!((bad >> (16 * c + 15)) & 1u)) continue;
+              const float x = none ? __int_as_float(0x7fffffff) : half_of<T>(w, c);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (sound[e]) o[j][2 * e + c] = ((got >> (2 * j + c)) & 1u ? o[j][2 * e + c] : 0.f) + x;
+              got |= 1u << (2 * j + c);
+            }
+          }
+        }
+      }
       if (whole && last) {
         T* out = static_cast<T*>(p.out) +
                  (static_cast<long long>(cc.i) * p.nh + head * p.group + part * kRows) * D + 2 * t;
@@ -461,7 +503,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
       } else {
         // slot 0: a unit that an earlier share began (or that begins with this one); slot 1: one begun inside
         const long long piece = 2 * w_id + (f - cc.blk > f0 ? 1 : 0);
-        (void)last;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = g + 8 * e;
@@ -482,6 +523,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
     }
   }
 }
+
+// a piece's output by its factor; one that is not finite stays (the factor may have underflowed to 0)
+__device__ __forceinline__ float weighted(float a, float x) { return isfinite(x) ? a * x : x; }
 
 // One CTA for each share of the line: if its start is the first cut of a unit, the CTA joins that
 // unit's pieces.  A thread has four output elements of one head and, where there are fewer of
@@ -541,10 +585,10 @@ __global__ void __launch_bounds__(kJoinThreads, 12)
         const float4 x = reinterpret_cast<const float4*>(p.acc + (piece(k) * kept + r) * D)[v];
         const float a = ex2_approx(ml.x - m);
         l += a * ml.y;
-        acc.x += a * x.x;
-        acc.y += a * x.y;
-        acc.z += a * x.z;
-        acc.w += a * x.w;
+        acc.x += weighted(a, x.x);
+        acc.y += weighted(a, x.y);
+        acc.z += weighted(a, x.z);
+        acc.w += weighted(a, x.w);
       }
     }
     if (groups > 1) {   // the groups' sums, in their order
@@ -620,7 +664,7 @@ __global__ void __launch_bounds__(kHeadThreads)
     const float a = ex2_approx(ml.x - m);
     l += a * ml.y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += a * src[e];
+    for (int e = 0; e < E; ++e) acc[e] += weighted(a, src[e]);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];

@@ -284,3 +284,67 @@ def test_a_workspace_of_fewer_bytes_than_it_counts_is_refused():
         rpp.attention_decode(c, 0, q, workspace=torch.empty(1, dtype=torch.uint8, device=dev()).expand(n))
     with pytest.raises(rpp.RppError):
         rpp.attention_decode(c, 0, q, workspace=torch.empty(n - 1, dtype=torch.uint8, device=dev()))
+
+
+def put(c, kv, slot, j, head, col, x):
+    """One element of a sequence's K (kv 0) or V (1) row j in layer 0."""
+    ps = c.cfg.page_size
+    c.pool[0, int(c.table[slot, j // ps]), kv, head, j % ps, col] = x
+
+
+def same(a, b):
+    return ((a == b) | (torch.isnan(a) & torch.isnan(b))).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype,d,nh,nkv,lens", [
+    ("fp16", 64, 4, 4, [1, 2, 16, 17, 31, 40] * 40),          # a warp has them whole
+    ("bf16", 128, 20, 1, [1, 2, 16, 17, 31, 40] * 40),        # above 16 query heads
+    ("bf16", 128, 8, 2, [3000]),                              # cut, joined by query head
+    ("fp16", 64, 5, 1, [2, 5000, 1]),
+    ("fp16", 128, 8, 2, [700, 1, 333, 900] * 25),             # cut, joined by the cut
+    ("bf16", 64, 3, 3, [1200, 40] * 128),
+])
+def test_values_that_are_not_finite(dtype, d, nh, nkv, lens, bad):
+    """One element of one value row, first, in the middle or last in its sequence: the outputs of that
+    column in the heads that read it are it, every other one is as without it."""
+    c = make(dtype, lens, nkv, d, 16)
+    q = queries(len(lens), nh, d, dtype)
+    want = rpp.attention_decode(c, 0, q).clone()
+    for s, n in enumerate(lens):
+        put(c, 1, s, (0, n // 2, n - 1)[s % 3], nkv - 1, 5, bad)
+    want.view(len(lens), nkv, nh // nkv, d)[:, -1, :, 5] = bad
+    assert same(rpp.attention_decode(c, 0, q), want)
+    assert rpp.get_device_error(c.err) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 200, 2048])              # cut and joined by head, by cut; whole
+@pytest.mark.parametrize("dtype,far", [("fp16", 30.0), ("fp16", 130.0), ("bf16", 60.0), ("bf16", 130.0)])
+@pytest.mark.parametrize("first", [False, True])
+def test_an_infinite_value_of_a_small_weight(dtype, far, rows, first):
+    """The weight e^-far is above 0 whatever the arithmetic makes of it, so the output is the
+    infinity; with the infinite value's key before the largest one, too.  -inf as its score makes the
+    weight 0, and 0 times infinity is NaN."""
+    n, d = 1000, 64
+    c = make(dtype, [n], 1, d, 16, nan=False)
+    c.pool[0, :, 0] = 0
+    at = 3 if first else 997
+    for j in range(n):
+        if first and j > 900:
+            put(c, 0, 0, j, 0, 0, far)
+    if not first:
+        put(c, 0, 0, at, 0, 0, -far)
+    q = torch.zeros(rows, d, device=dev(), dtype=TDT[dtype])
+    q[:, 0] = 8.0
+    slots = torch.zeros(rows, dtype=torch.int32, device=dev())
+    base = rpp.attention_decode(c, 0, q, slots).clone()
+    assert torch.isfinite(base.float()).all()
+    put(c, 1, 0, at, 0, 7, float("inf"))
+    put(c, 1, 0, at, 0, 8, float("-inf"))
+    put(c, 1, 0, at, 0, 9, float("inf"))
+    put(c, 1, 0, at + 1, 0, 9, float("-inf"))
+    base[:, 7], base[:, 8], base[:, 9] = float("inf"), float("-inf"), float("nan")
+    assert same(rpp.attention_decode(c, 0, q, slots), base)
+    put(c, 0, 0, at, 0, 0, float("-inf"))
+    got = rpp.attention_decode(c, 0, q, slots)
+    assert torch.isnan(got[:, 7:10]).all() and torch.isfinite(got[:, 10:].float()).all()
