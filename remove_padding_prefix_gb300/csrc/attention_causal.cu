@@ -42,8 +42,8 @@
 // What a row must not see stays out of it: scores past the row become -inf before the
 // maximum.  P is 0 there, but 0 * inf is not, so in the tiles on the diagonal V rows past
 // the sequence are zeroed in shared memory, and elements of V that are not finite are
-// taken out before the product and added back to the rows that may see them (their sums
-// with positive weights are the elements themselves).  Two warps do that for every V tile
+// taken out before the product; the outputs of the rows that see them are written from V once
+// more (their sums with positive weights are the elements themselves).  Two warps do that for every V tile
 // before the product may read it, so their wait on a ring slot is never a phase off.  Every mbarrier wait is bounded; a
 // wait that gives up records RPP_DERR_TIMEOUT and the CTA drains, frees tensor memory
 // and exits.
@@ -84,7 +84,7 @@ struct Shape {
   static constexpr uint32_t kOffStage = kOffRing + kSlots * kTileBytes;   // 2 KB a softmax warp: rows on their way out
   static constexpr uint32_t kOffBar = kOffStage + kStreams * 4 * 2048;
   static constexpr uint32_t kOffMisc = kOffBar + kStreams * 32 * 8;
-  static constexpr uint32_t kOffList = kOffMisc + 32;
+  static constexpr uint32_t kOffList = kOffMisc + 64;
 };
 // Registers: launched with 128 a thread, 32768 a stream (checked at the first launch: a split above
 // what the launch has would wait for ever); 128 threads keep 80, the softmax's 128 take 176.
@@ -269,14 +269,16 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   int* s_status = reinterpret_cast<int*>(smem + S::kOffMisc + 8);
-  volatile int* met = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 12);   // V held an element that is not finite
+  // [8] of the item of round r, in met[r % 8]: r + 1 where its diagonal V tile held an element that is not finite.
+  // (The watch of V is at most three items ahead of the softmax, whose O has to be free for the next PV.)
+  volatile int* met = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 32);
   const int warp = warp_id() & 7, lane = lane_id();   // warp of the stream
 
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    *met = 0;
+    for (int i = 0; i < 8; ++i) met[i] = 0;
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], S::kStreams);
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
       // ------------------------------------------------------------ V: what some queries must not see
       // Every V tile passes here on its way to the product.  In a tile that reaches past the
       // item's first query, rows past the sequence become zero, and elements that are not finite
-      // are taken out and the fact noted for good.
+      // are taken out and the fact noted for the item.
       const int t = (warp - 2) * 32 + lane;
       uint32_t nv = 0;                               // V tiles passed
       bool ok = true;
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
                   f |= nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w);
                 }
                 if (f & 0x80008000u) {
-                  *met = 1;
+                  met[r & 7] = r + 1;
 #pragma unroll 1
                   for (int c = 0; c < HB * 8; ++c) {
                     const uint4 x = *chunk(c);
@@ -538,7 +540,6 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
     // ------------------------------------------------------------ softmax: one thread a query row
     const int quad = warp & 3;                     // tensor-memory lanes of this warp
-    const int row = quad * 32 + lane;              // query of the tile, and V row of a diagonal tile
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t t_p = t_s + S::kColP, t_o = t_s + S::kColO;
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
@@ -764,18 +765,41 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
         }
         __syncwarp();
       }
-      // Elements that were taken out of the diagonal tile are added back, from memory, to the rows that
-      // see them: such an output is not finite either, so nothing is lost in adding it to the rounded
-      // one.  (The note is visible here: o_full came after the v_ready of that tile.)
-      if (*met != 0 && it.q0 + row < it.len) {
-        T* mine = out + (it.c0 + it.q0 + row) * pitch + it.h * D;   // stored by this warp, before a __syncwarp
+      // V elements that are not finite were taken out of the diagonal tile: a column that has one up to a row's
+      // own key is there the sum of such elements, which needs neither weights nor the finite rest.  The
+      // warp goes through V's rows in order, a lane with D / 32 columns, and writes what its rows have
+      // by then.  (The note is visible here: o_full came after the v_ready of that tile.)
+      if (live && met[(r - 1) & 7] == r) {
+        constexpr int E = D / 32;                      // columns of a lane
+        constexpr int U = D / 16;                      // rows at a time: twice as many would spill
+        const T* vr = v_rows + static_cast<long long>(it.c0) * kv_stride + it.h / group * D + lane * E;
+        T* o = out + static_cast<long long>(it.c0) * pitch + it.h * D + lane * E;
+        const int own = it.q0 + quad * 32, end = min(own + 32, it.len);
+        // rows whose sum is a number (elsewhere the whole row is NaN)
+        const uint32_t sound = __ballot_sync(0xffffffffu, l > 0.f && l < __int_as_float(0x7f800000));
+        float sum[E] = {};
+        uint32_t got = 0;                              // columns that have one
 #pragma unroll 1
-        for (int k = it.q0; k <= it.q0 + row; ++k) {
-          const T* vr = v_rows + static_cast<long long>(it.c0 + k) * kv_stride + it.h / group * D;
-#pragma unroll 1
-          for (int e = 0; e < D; ++e) {
-            const float f = to_f32(vr[e]);
-            if (!isfinite(f)) mine[e] = from_f32<T>(to_f32(mine[e]) + f);
+        for (int k0 = 0; k0 < end; k0 += U) {          // own is a multiple of U
+          uint32_t w[U][E / 2];
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+              w[k][e] = k0 + k < end ? *reinterpret_cast<const uint32_t*>(vr + static_cast<long long>(k0 + k) * kv_stride + 2 * e) : 0u;
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              if (!((nonfinite2<T>(w[k][e / 2]) >> (16 * (e & 1) + 15)) & 1u)) continue;
+              sum[e] += half_of<T>(w[k][e / 2], e & 1);
+              got |= 1u << e;
+            }
+            if (k0 >= own && k0 + k < end && ((sound >> (k0 + k - own)) & 1u)) {
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if ((got >> e) & 1u) o[(k0 + k) * pitch + e] = from_f32<T>(sum[e]);
+            }
           }
         }
       }

@@ -312,3 +312,30 @@ def test_two_streams_at_once():
         assert rpp.get_device_error(err) == 0
         check_rows(got[0], q, k, v, cu, nh, nkv, d)
         assert all(torch.equal(got[0], g) for g in got)
+
+
+def test_a_value_that_is_not_finite_costs_its_own_rows_only():
+    """One infinity in the first of 64 prompts: the others take their time as before.  (Noted for good, it
+    made every later item of a CTA look through its diagonal rows: 34 times the time of the batch.)"""
+    lens = [int(x) for x in np.random.default_rng(1).integers(32, 385, 64)]
+    q, k, v = make(lens, 16, 16, 64, "bf16")
+    a = (ints(cu_of(lens)), 64, 384, 16, 16, 64)
+    out = torch.empty(q.shape[0], 16 * 64, dtype=torch.bfloat16, device=dev())
+
+    def best():
+        ts = []
+        for _ in range(12):
+            s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            s.record()
+            for _ in range(20):
+                rpp.attention_causal_varlen(q, k, v, *a, out=out)
+            e.record()
+            e.synchronize()
+            ts.append(s.elapsed_time(e))
+        return min(ts[2:])
+
+    plain = best()
+    v[0, 3] = float("inf")
+    spoilt = best()
+    assert (out[0:lens[0], 3] == float("inf")).all()
+    assert spoilt <= 2 * plain, (spoilt, plain)
