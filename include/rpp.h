@@ -544,7 +544,8 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  * sequence b (rows cu[b] .. cu[b+1]-1) and head h
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j]) v[j],  cu[b] <= j <= i,
  * k and v of kv head h / (nh / nkv).  Rows that a query must not see have no effect on
- * it, whatever they hold (infinities and NaN among it).
+ * it, whatever they hold (infinities and NaN among it); a value that it sees and that is not finite
+ * gives what the formula does, a weight being above 0, however small, but for a score of -inf.
  *  q       device rows of nh * d of dtype, q_stride elements apart; k, v: rows of nkv * d,
  *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
  *          QKV projection's output); T_max <= 2^31 - 65536 rows each

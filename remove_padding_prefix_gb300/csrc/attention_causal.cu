@@ -43,7 +43,9 @@
 // maximum.  P is 0 there, but 0 * inf is not, so in the tiles on the diagonal V rows past
 // the sequence are zeroed in shared memory, and elements of V that are not finite are
 // taken out before the product; the outputs of the rows that see them are written from V once
-// more (their sums with positive weights are the elements themselves).  Two warps do that for every V tile
+// more (their sums with positive weights are the elements themselves), and so are outputs that a weight
+// of 0 times an infinity in an earlier tile made NaN (looking for them: 42.7 against 41.8 us on the short
+// prompts above).  Two warps do that for every V tile
 // before the product may read it, so their wait on a ring slot is never a phase off.  Every mbarrier wait is bounded; a
 // wait that gives up records RPP_DERR_TIMEOUT and the CTA drains, frees tensor memory
 // and exits.
@@ -241,7 +243,7 @@ template <typename T, int D, bool PAIR>
 __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
     attention_causal_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, int q_x, int k_x, int v_x,
-                            const T* __restrict__ v_rows, int kv_stride, const int32_t* __restrict__ cu, int B,
+                            const T* __restrict__ k_rows, const T* __restrict__ v_rows, int kv_stride, const int32_t* __restrict__ cu, int B,
                             int T_max, int max_len, int nh, int group, int classes, T* __restrict__ out,
                             float scale_log2, int32_t* err) {
   using S = Shape<D, PAIR>;
@@ -736,7 +738,19 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
+      // rows whose sum is a number: all their scores are, or -inf (elsewhere the whole row is NaN)
+      const bool number = l > 0.f && l < __int_as_float(0x7f800000);
+      bool nan_seen = false;                         // outputs that are NaN all the same (one tile: V is looked over)
+      if (nt > 1) {
+        float nan[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < D; e += 2)
+          nan[e / 2 & 3] = max3_nan(nan[e / 2 & 3], __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]));
+        const float one = max3_nan(max3_nan(nan[0], nan[1], nan[2]), nan[3], 0.f);
+        nan_seen = __any_sync(0xffffffffu, number && one != one && it.q0 + quad * 32 + lane < it.len);
+      }
       const float inv = __fdividef(1.0f, l);
+      const uint64_t inv2 = f2_pack(inv, inv);
       // A thread has a row, a store wants whole lines: 32 columns at a time through 2 KB of shared
       // memory of the warp's own (16-byte chunk u of row r at u ^ (r / 2 & 3): no bank conflict
       // either way), then four lanes a row.
@@ -751,9 +765,11 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
         for (int u = 0; u < 4; ++u) {
           uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack2<T>(__uint_as_float(ov[32 * c + 8 * u + 2 * e]) * inv,
-                            __uint_as_float(ov[32 * c + 8 * u + 2 * e + 1]) * inv);
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(ov[32 * c + 8 * u + 2 * e]),
+                                               __uint_as_float(ov[32 * c + 8 * u + 2 * e + 1])), inv2);
+            w[e] = pack2<T>(f2_lo(x2), f2_hi(x2));
+          }
           *reinterpret_cast<uint4*>(mine + ((u ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
@@ -765,18 +781,19 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
         }
         __syncwarp();
       }
-      // V elements that are not finite were taken out of the diagonal tile: a column that has one up to a row's
-      // own key is there the sum of such elements, which needs neither weights nor the finite rest.  The
-      // warp goes through V's rows in order, a lane with D / 32 columns, and writes what its rows have
-      // by then.  (The note is visible here: o_full came after the v_ready of that tile.)
-      if (live && met[(r - 1) & 7] == r) {
+      // V elements that are not finite: a column that has one up to a row's own key is there the sum of such
+      // elements, which needs neither weights nor the finite rest.  They were taken out of the diagonal tile,
+      // and before it a weight that underflowed to 0 made NaN of one (nonfinite.cuh).  Where that
+      // happened the warp goes through V's rows in order, a lane with D / 32 columns, and writes what its rows
+      // have by then.  (The note is visible here: o_full came after the v_ready of that tile.)
+      if (live && (nan_seen || met[(r - 1) & 7] == r)) {
         constexpr int E = D / 32;                      // columns of a lane
         constexpr int U = D / 16;                      // rows at a time: twice as many would spill
-        const T* vr = v_rows + static_cast<long long>(it.c0) * kv_stride + it.h / group * D + lane * E;
+        const long long first = static_cast<long long>(it.c0) * kv_stride + it.h / group * D + lane * E;
+        const T *kr = k_rows + first, *vr = v_rows + first;
         T* o = out + static_cast<long long>(it.c0) * pitch + it.h * D + lane * E;
         const int own = it.q0 + quad * 32, end = min(own + 32, it.len);
-        // rows whose sum is a number (elsewhere the whole row is NaN)
-        const uint32_t sound = __ballot_sync(0xffffffffu, l > 0.f && l < __int_as_float(0x7f800000));
+        const uint32_t sound = __ballot_sync(0xffffffffu, number);
         float sum[E] = {};
         uint32_t got = 0;                              // columns that have one
 #pragma unroll 1
@@ -789,11 +806,16 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
               w[k][e] = k0 + k < end ? *reinterpret_cast<const uint32_t*>(vr + static_cast<long long>(k0 + k) * kv_stride + 2 * e) : 0u;
 #pragma unroll
           for (int k = 0; k < U; ++k) {
+            uint32_t bad = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              if (!((nonfinite2<T>(w[k][e / 2]) >> (16 * (e & 1) + 15)) & 1u)) continue;
-              sum[e] += half_of<T>(w[k][e / 2], e & 1);
-              got |= 1u << e;
+            for (int e = 0; e < E; ++e) bad |= ((nonfinite2<T>(w[k][e / 2]) >> (16 * (e & 1) + 15)) & 1u) << e;
+            if (__any_sync(0xffffffffu, bad != 0)) {
+              // a K row that is not finite has the score -inf in a sound row: weight 0, and 0 * inf is NaN
+              const bool none = __any_sync(0xffffffffu, part_nonfinite<T, D>(kr + static_cast<long long>(k0 + k) * kv_stride));
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if ((bad >> e) & 1u) sum[e] += none ? __int_as_float(0x7fffffff) : half_of<T>(w[k][e / 2], e & 1);
+              got |= bad;
             }
             if (k0 >= own && k0 + k < end && ((sound >> (k0 + k - own)) & 1u)) {
 #pragma unroll
@@ -840,7 +862,7 @@ cudaError_t launch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
   const long long room = (PAIR ? 1LL : 2LL) * num_sms();
   const int grid = static_cast<int>(most < room ? most : room);
   return launch_pdl(attention_causal_kernel<T, D, PAIR>, dim3(grid), dim3(S::kThreads), smem, stream, t.q, t.k, t.v,
-                    t.q_x, t.k_x, t.v_x, static_cast<const T*>(a.v), a.kv_stride, a.cu, a.B, a.T_max, a.max_len, a.nh,
+                    t.q_x, t.k_x, t.v_x, static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.kv_stride, a.cu, a.B, a.T_max, a.max_len, a.nh,
                     a.nh / a.nkv, classes, static_cast<T*>(a.out), a.scale * 1.4426950408889634f, a.err);
 }
 

@@ -314,6 +314,49 @@ def test_two_streams_at_once():
         assert all(torch.equal(got[0], g) for g in got)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh,dtype,far", [(1, "fp16", 30.0), (2, "fp16", 130.0), (1, "bf16", 130.0), (2, "bf16", 60.0)])
+def test_an_infinite_value_of_a_small_weight(d, nh, dtype, far):
+    """A value before the diagonal tile (and in it) whose weight e^-far is above 0 whatever the arithmetic
+    makes of it: the rows that see it answer the infinity, those that see both infinities NaN.  A score
+    of -inf makes the weight 0, and 0 times infinity is NaN."""
+    lens = [500, 300]
+    q, k, v = make(lens, nh, 1, d, dtype, seed=3)
+    q.zero_()
+    q[:, ::d] = 8.0
+    k.zero_()
+    k[5, 0] = k[9, 0] = k[390, 0] = -far
+    a = (ints(cu_of(lens)), 2, 500, nh, 1, d)
+    err = rpp.new_error_word()
+    base = rpp.attention_causal_varlen(q, k, v, *a, scale=0.125, err=err)
+    assert torch.isfinite(base.float()).all()
+    inf = float("inf")
+    v[5, 3] = inf
+    v[9, 4] = -inf
+    v[5, 6] = inf
+    v[9, 6] = -inf
+    v[390, 8] = inf
+    got = rpp.attention_causal_varlen(q, k, v, *a, scale=0.125, err=err)
+    k[5, 0] = -inf
+    k[390, 0] = -inf
+    dropped = rpp.attention_causal_varlen(q, k, v, *a, scale=0.125, err=err)
+    assert rpp.get_device_error(err) == 0
+
+    def same(x, y):
+        return ((x == y) | (torch.isnan(x) & torch.isnan(y))).all()
+
+    for h in range(nh):
+        want = base[:, h * d:(h + 1) * d].clone()
+        want[5:500, 3], want[9:500, 4], want[5:9, 6], want[9:500, 6], want[390:500, 8] = inf, -inf, inf, float("nan"), inf
+        x = got[:, h * d:(h + 1) * d]
+        assert same(x[:, [3, 4, 6, 8]], want[:, [3, 4, 6, 8]])
+        keep = [e for e in range(d) if e not in (3, 4, 6, 8)]
+        assert torch.equal(x[:, keep], want[:, keep])
+        x = dropped[:, h * d:(h + 1) * d]
+        assert torch.isnan(x[5:500, 3]).all() and torch.isnan(x[390:500, 8]).all() and (x[9:500, 4] == -inf).all()
+        assert torch.isfinite(x[:, keep].float()).all() and torch.equal(x[500:], want[500:])
+
+
 def test_a_value_that_is_not_finite_costs_its_own_rows_only():
     """One infinity in the first of 64 prompts: the others take their time as before.  (Noted for good, it
     made every later item of a CTA look through its diagonal rows: 34 times the time of the batch.)"""
