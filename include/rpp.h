@@ -470,10 +470,11 @@ RPP_API rpp_status rpp_patch_merge_forward(const rpp_merge_cfg* cfg, const void*
  * Lists of slots are device int32[n], 1 <= n <= 4096.  `err` is required by the calls that change
  * a cache.  A slot out of range, or given twice to reserve, append, fork (destinations) or free,
  * records RPP_DERR_SLOT and changes nothing.  reserve changes nothing on any error, fork on any
- * but RPP_DERR_PAGE (a source whose table names pages outside the pool); the others skip
- * the sequence (or row) whose length or page is wrong, record RPP_DERR_LENGTH or RPP_DERR_PAGE,
- * and stay in bounds.  Of what such a fork, append or free has yet to do when the word is set,
- * for other sequences too, any part may be left out; a compaction is carried out for them.
+ * but RPP_DERR_PAGE (a source whose table names pages outside the pool: the wrong numbers go with the
+ * copy); the others skip the sequence (or row) whose length or page is wrong, record RPP_DERR_LENGTH
+ * or RPP_DERR_PAGE, and stay in bounds.  Such a fork or compaction is carried out for the other
+ * sequences; of what such an append or free has yet to do for them when the word is set, any part may
+ * be left out (the same call does it once the word is cleared).
  * Calls on one cache are ordered by their stream; a cache is not to be changed on one
  * stream while another reads it.
  * ------------------------------------------------------------------------------ */

@@ -104,11 +104,18 @@ __device__ __forceinline__ int2 warp_stretch(int pages) {
 // length and, where from[i] ends inside a page, a page of its own for that end (the
 // pages, the table row and the reference counts of the shared part follow in
 // fork_copy_kernel).  All or nothing: any error leaves the state as it was.
+// That the fork is on is left for fork_copy_kernel in the state itself, the error word being anybody's:
+// kForkMark in the first table entry of a destination that shares pages, and `shares` times
+// kForkShare on the count of its own page, one for each CTA that copies a part of it.
 // Shared memory: int32 need[n + 1] (then its exclusive scan), the slot bitmap.
+constexpr int kForkMark = -0x7fffffff - 1;
+constexpr int kForkShare = 1 << 17;   // above every count: a page has at most kKvMaxSlots users
+constexpr int kMostShares = 8192;     // kMostShares * kForkShare + 1 is an int
+static_assert(kForkShare > kKvMaxSlots && static_cast<long long>(kMostShares) * kForkShare < 0x7fffffffLL, "");
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads)
     kv_reserve_kernel(KvDims d, int32_t* __restrict__ table, int32_t* __restrict__ lens, int32_t* __restrict__ refs,
-                      const int32_t* __restrict__ slots, const int32_t* __restrict__ counts_or_from, int n,
+                      const int32_t* __restrict__ slots, const int32_t* __restrict__ counts_or_from, int n, int shares,
                       int32_t* err) {
   extern __shared__ int32_t s_need[];
   uint32_t* seen = reinterpret_cast<uint32_t*>(s_need + n + 1);
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int s = slots[lo];
         const int first = kFork ? lens[counts_or_from[lo]] / d.page_size : used_pages(lens[s], d.page_size);
         table[static_cast<long long>(s) * d.max_pages + first + (rank - s_need[lo])] = p + e;
-        refs[p + e] = 1;
+        refs[p + e] = kFork ? 1 + shares * kForkShare : 1;
       }
       ++rank;
     }
@@ -223,7 +230,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int s = slots[i];
     if constexpr (kFork) {
-      lens[s] = lens[counts_or_from[i]];
+      const int len = lens[counts_or_from[i]];
+      lens[s] = len;
+      if (len >= d.page_size) table[static_cast<long long>(s) * d.max_pages] = kForkMark;
     } else {
       lens[s] += counts_or_from[i];
     }
@@ -233,27 +242,32 @@ __global__ void __launch_bounds__(kPlanThreads)
 // The shared part of each fork (table entries, reference counts) and the rows of its own
 // last page, in all layers.  blockIdx.x: pairs, grid-strided; blockIdx.y: shares of a pair's rows.  A pair's copy is
 // r rows (those past the last whole page) of d * 2 bytes in each of layers * 2 * kv heads
-// places; only those rows are moved.
+// places; only those rows are moved.  What there is to do stands in the plan's marks, each taken away by
+// who has done it, so a wrong page number in one source (recorded) leaves the other pairs alone,
+// and a call that the plan refused finds no marks, whatever its lists and the state hold.
 __global__ void __launch_bounds__(kMoveThreads)
     kv_fork_copy_kernel(KvDims d, uint4* __restrict__ pool, int32_t* __restrict__ table,
                         const int32_t* __restrict__ lens, int32_t* __restrict__ refs, const int32_t* __restrict__ from,
                         const int32_t* __restrict__ to, int n, int32_t* err) {
-  __shared__ int s_flag;
   pdl_wait();
   pdl_trigger();
-  // the plan refused the call, or an earlier kernel failed.  This launch's own CTAs set the
-  // word only for a corrupt table; the CTAs that start after that stop there.
-  if (quit(err, &s_flag)) return;
   const int vpr = d.head_dim / 8;                                   // 16-byte vectors of a row
   const long long page_vec = 2LL * d.kv_heads * d.page_size * vpr;  // of a page in one layer
   const long long layer_vec = page_vec * d.pages;
   const int head_vec = d.page_size * vpr;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int len = lens[to[i]];
+    const int a = from[i], b = to[i];
+    if (a < 0 || a >= d.slots || b < 0 || b >= d.slots) continue;   // (the same for all threads, as what follows)
+    const int len = lens[b];
+    if (!len_ok(len, d)) continue;
     const int full = len / d.page_size, rows = len % d.page_size;
-    const int32_t* trow_from = table + static_cast<long long>(from[i]) * d.max_pages;
-    int32_t* trow_to = table + static_cast<long long>(to[i]) * d.max_pages;
-    if (blockIdx.y == 0) {
+    const int32_t* trow_from = table + static_cast<long long>(a) * d.max_pages;
+    int32_t* trow_to = table + static_cast<long long>(b) * d.max_pages;
+    const int pa = rows ? trow_from[full] : -1, pb = rows ? trow_to[full] : -1;
+    const bool share = blockIdx.y == 0 && full > 0 && trow_to[0] == kForkMark;
+    const bool copy = pb >= 0 && pb < d.pages && refs[pb] >= kForkShare;
+    __syncthreads();   // the marks are read
+    if (share) {
       for (int j = threadIdx.x; j < full; j += blockDim.x) {
         const int p = trow_from[j];
         trow_to[j] = p;
@@ -261,10 +275,12 @@ __global__ void __launch_bounds__(kMoveThreads)
         else set_device_error(err, RPP_DERR_PAGE);
       }
     }
-    if (rows == 0) continue;
-    const int pa = trow_from[full], pb = trow_to[full];
-    if (pa < 0 || pa >= d.pages || pb < 0 || pb >= d.pages) {
-      if (threadIdx.x == 0) set_device_error(err, RPP_DERR_PAGE);
+    if (!copy) continue;
+    if (pa < 0 || pa >= d.pages) {
+      if (threadIdx.x == 0) {
+        set_device_error(err, RPP_DERR_PAGE);
+        atomicSub(&refs[pb], kForkShare);
+      }
       continue;
     }
     const uint4* src = pool + pa * page_vec;
@@ -294,6 +310,7 @@ __global__ void __launch_bounds__(kMoveThreads)
       for (int u = 0; u < U; ++u)
         if (at[u] >= 0) dst[at[u]] = x[u];
     }
+    if (threadIdx.x == 0) atomicSub(&refs[pb], kForkShare);
   }
 }
 
@@ -580,21 +597,22 @@ cudaError_t launch_kv_reserve(const KvDims& d, const KvState& c, const int32_t* 
                               int32_t* err, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(n) + 1 + (d.slots + 31) / 32) * 4;
   return launch_pdl(kv_reserve_kernel<false>, dim3(1), dim3(kPlanThreads), smem, stream, d, c.table, c.lens, c.refs,
-                    slots, counts, n, err);
+                    slots, counts, n, 0, err);
 }
 
 cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* from, const int32_t* to, int n,
                            int32_t* err, cudaStream_t stream) {
-  const size_t smem = (static_cast<size_t>(n) + 1 + (d.slots + 31) / 32) * 4;
-  const cudaError_t e = launch_pdl(kv_reserve_kernel<true>, dim3(1), dim3(kPlanThreads), smem, stream, d, c.table,
-                                   c.lens, c.refs, to, from, n, err);
-  if (e != cudaSuccess) return e;
   // More CTAs than fit at once: the pairs' last pages are full to different degrees, and a share of
   // an empty one costs a CTA's start only.  16 prompts forked 8 times over 12 layers, with the free
   // before it: 71 us at 8 CTAs an SM, 64 at 32, 71 at 64, 87 at 128.
   const long long vec = static_cast<long long>(d.layers) * 2 * d.kv_heads * (d.page_size - 1) * (d.head_dim / 8);
   const int x = blocks_for(n, 32 * num_sms());
-  const int y = blocks_for(vec / (4 * kMoveThreads) + 1, (32 * num_sms() + x - 1) / x);
+  const int most = (32 * num_sms() + x - 1) / x;
+  const int y = blocks_for(vec / (4 * kMoveThreads) + 1, most < kMostShares ? most : kMostShares);
+  const size_t smem = (static_cast<size_t>(n) + 1 + (d.slots + 31) / 32) * 4;
+  const cudaError_t e = launch_pdl(kv_reserve_kernel<true>, dim3(1), dim3(kPlanThreads), smem, stream, d, c.table,
+                                   c.lens, c.refs, to, from, n, y, err);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kv_fork_copy_kernel, dim3(x, y), dim3(kMoveThreads), 0, stream, d, static_cast<uint4*>(c.pool),
                     c.table, static_cast<const int32_t*>(c.lens), c.refs, from, to, n, err);
 }

@@ -407,3 +407,43 @@ def test_compact_with_one_corrupt_table_entry_moves_the_others():
         new = table[s, :used].long()
         assert (new < n).all() and (new >= 0).all()
         assert torch.equal(words_t(p.gpu.pool[:, new]), words_t(pool[:, row[:used].long()]))
+
+
+def test_fork_with_one_corrupt_source_carries_out_the_others():
+    """Page numbers outside the pool in two of the sources, and more pairs than CTAs that run at once: every
+    other destination is as the oracle has it, and so are all lengths and the counts of all pages."""
+    n = 3000
+    p = Pair(1, 9000, 4, 1, 8, 2 * n, 4)
+    held = list(range(40))
+    p.grow(held, [4 * (s % 3) + 1 + s % 4 for s in held])
+    p.check()
+    src = [int(x) for x in np.random.default_rng(2).integers(0, 40, n)]
+    src[:2] = [10, 5]                                     # of 7 rows and 10: a whole page and a part, two and a part
+    dst = list(range(n, 2 * n))
+    assert (p.ref.lens[10], p.ref.lens[5]) == (7, 10)
+    whole = p.ref.rows[5][0]
+    p.gpu.table[5, 0] = 9000
+    p.gpu.table[10, 1] = -7
+    before = p.ref.pool.copy()
+    p.fork(src, dst)
+    p.ref.refs[whole] = 1                                 # nobody could share it
+    for s, t in [(s, s) for s in held] + list(zip(src, dst)):
+        if s == 5:
+            p.ref.rows[t][0] = 9000                       # the wrong number goes with the copy
+        if s == 10 and t != s:                            # a page of its own, with no rows to copy
+            own = p.ref.rows[t][1]
+            p.ref.pool[:, own] = before[:, own]
+    p.ref.rows[10][1] = -7
+    p.check(od.PAGE)
+
+
+def test_a_refused_fork_leaves_forks_of_before_alone():
+    """Again the same fork: the destinations are not empty, and what they have written since stays."""
+    p = _some()
+    p.fork([0], [2])
+    k, v, kw, vw = p.rows(1)
+    rpp.kv_append(p.gpu, 0, k, v, ints([2]))
+    p.ref.append(0, kw, vw, [2], [1])
+    p.check()
+    rpp.kv_fork(p.gpu, ints([0]), ints([2]))
+    p.check(od.SLOT)
