@@ -511,8 +511,9 @@ RPP_API rpp_status rpp_kv_reserve(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  *              slots[i], in order; NULL: one row each (rows_max >= n).  Rows from cu[n] on
  *              are not read.
  * The rows go to positions lens - count .. lens - 1, reserved before (once for all layers).
- * RPP_DERR_LENGTH: more rows than the sequence has tokens, or a row before cu[0]; RPP_DERR_PAGE:
- * a page that is shared with another sequence; RPP_DERR_ROWS: cu[n] > rows_max. */
+ * RPP_DERR_LENGTH: cu[i + 1] < cu[i] (nothing is written), more rows than the sequence has tokens, or a
+ * row before cu[0]; RPP_DERR_PAGE: a page that is shared with another sequence; RPP_DERR_ROWS: cu[n] > rows_max
+ * or cu[0] < 0. */
 RPP_API rpp_status rpp_kv_append(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* k,
                                  const void* v, int row_stride, const int32_t* slots, const int32_t* cu_seqlens, int n,
                                  int rows_max, int32_t* err, rpp_stream stream);

@@ -49,18 +49,20 @@ __device__ __forceinline__ int warp_scan_incl(int v) {
 
 // The first words of a kernel that takes a list of slots: one reading of the error word for the
 // whole CTA (other CTAs may set it at any time) and the list against the cache.  False if the CTA must
-// quit: the word is set, or a slot lies outside [0, d.slots) or is given twice (recorded by one
-// thread; every CTA of a launch comes to the same answer).  `seen`: (d.slots + 31) / 32 words of shared
-// memory, left holding the slots given; first: slots[threadIdx.x], read ahead by the caller so
-// that the readings travel together.  Holds __syncthreads: called by all threads.
+// quit: the word is set, or a slot lies outside [0, d.slots) or is given twice, or cu[i + 1] < cu[i]
+// (recorded by one thread; every CTA of a launch comes to the same answer).  `seen`: (d.slots + 31) / 32
+// words of shared memory, left holding the slots given; cu: [n + 1] or null; first, c0, c1: slots[threadIdx.x]
+// and cu[threadIdx.x], cu[threadIdx.x + 1], read ahead by the caller so that the readings travel together.
+// Holds __syncthreads: called by all threads.
 struct Gate {
-  int quit, bad;
+  int quit, bad, back;
 };
 __device__ __forceinline__ bool pass(const int32_t* __restrict__ slots, int n, int first, const KvDims& d,
-                                     uint32_t* seen, Gate* g, int32_t* err) {
+                                     uint32_t* seen, Gate* g, int32_t* err, const int32_t* __restrict__ cu = nullptr,
+                                     int c0 = 0, int c1 = 0) {
   if (threadIdx.x == 0) {
     g->quit = device_error_set(err) ? 1 : 0;
-    g->bad = 0;
+    g->bad = g->back = 0;
   }
   for (int i = threadIdx.x; i < (d.slots + 31) / 32; i += blockDim.x) seen[i] = 0u;
   __syncthreads();
@@ -68,10 +70,11 @@ __device__ __forceinline__ bool pass(const int32_t* __restrict__ slots, int n, i
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int s = i == static_cast<int>(threadIdx.x) ? first : slots[i];
     if (s < 0 || s >= d.slots || ((atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u)) g->bad = 1;
+    if (cu && (i == static_cast<int>(threadIdx.x) ? c1 < c0 : cu[i + 1] < cu[i])) g->back = 1;
   }
   __syncthreads();
-  if (g->bad && threadIdx.x == 0) set_device_error(err, RPP_DERR_SLOT);
-  return g->bad == 0;
+  if ((g->bad || g->back) && threadIdx.x == 0) set_device_error(err, g->bad ? RPP_DERR_SLOT : RPP_DERR_LENGTH);
+  return !g->bad && !g->back;
 }
 
 // One reading of the error word for the whole CTA.
@@ -369,9 +372,11 @@ __global__ void __launch_bounds__(kMoveThreads)
   pdl_wait();
   pdl_trigger();
   const int first = static_cast<int>(threadIdx.x) < n ? slots[threadIdx.x] : 0;
-  const int T = cu ? cu[n] : n;
-  if (!pass(slots, n, first, d, s_seen, &gate, err)) return;
-  if (T < 0 || T > rows_max) {
+  const int T = cu ? cu[n] : n, start = cu ? cu[0] : 0;
+  const bool mine = cu && static_cast<int>(threadIdx.x) < n;
+  const int c0 = mine ? cu[threadIdx.x] : 0, c1 = mine ? cu[threadIdx.x + 1] : 0;
+  if (!pass(slots, n, first, d, s_seen, &gate, err, cu, c0, c1)) return;
+  if (start < 0 || T > rows_max) {
     if (threadIdx.x == 0) set_device_error(err, RPP_DERR_ROWS);
     return;
   }

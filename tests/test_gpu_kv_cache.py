@@ -447,3 +447,25 @@ def test_a_refused_fork_leaves_forks_of_before_alone():
     p.check()
     rpp.kv_fork(p.gpu, ints([0]), ints([2]))
     p.check(od.SLOT)
+
+
+@pytest.mark.parametrize("cu,code", [([0, 5, 3, 8], od.LENGTH), ([0, 8, 5, 5], od.LENGTH), ([0, 2, 2, 1], od.LENGTH),
+                                     ([-2, 3, 4, 5], od.ROWS)])
+def test_append_with_cu_seqlens_that_step_back(cu, code):
+    """A negative count, as for reserve, or rows before the first: nothing is written."""
+    p = Pair(1, 12, 16, 2, 64, 4, 5)
+    p.grow([0, 1, 2], [20, 20, 20])
+    k, v, _, _ = p.rows(40)
+    rpp.kv_append(p.gpu, 0, k, v, ints([0, 1, 2]), ints(cu))
+    p.check(code)
+
+
+def test_append_with_a_step_back_far_down_the_list():
+    n = 1000
+    p = Pair(1, 1100, 2, 1, 8, n, 2)
+    p.grow(list(range(n)), [2] * n)
+    k, v, _, _ = p.rows(n)
+    cu = list(range(n + 1))
+    cu[700] -= 2
+    rpp.kv_append(p.gpu, 0, k, v, ints(list(range(n))), ints(cu))
+    p.check(od.LENGTH)
