@@ -552,7 +552,7 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
  *          QKV projection's output); T_max <= 2^31 - 65536 rows each
  *  out     device [T_max, nh * d] of dtype; rows >= cu[B] untouched; may alias none of q, k, v
- * d 64 or 128; dtype RPP_F16 or RPP_BF16; nh % nkv == 0; scale > 0 and finite; B <= 4096; every length <= max_len <=
+ * d 64 or 128; dtype RPP_F16 or RPP_BF16; nh % nkv == 0; 0 < scale <= 2e38; B <= 4096; every length <= max_len <=
  * 262144 (RPP_DERR_LENGTH; RPP_DERR_ROWS if cu[B] > T_max). */
 RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, const void* v, int q_stride,
                                                int kv_stride, const int32_t* cu_seqlens, int B, int T_max,
@@ -571,7 +571,7 @@ RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, con
  *  workspace  device, 256-byte aligned, >= rpp_attention_decode_workspace_bytes(cfg, n, nh)
  *             bytes, needs no initial contents; not shared by calls that may overlap
  * head_dim 64 or 128, page_size % 16 == 0 (RPP_EUNSUPPORTED otherwise), nh % kv_heads == 0,
- * n <= 4096, scale > 0 and finite. */
+ * n <= 4096, 0 < scale <= 2e38. */
 RPP_API size_t rpp_attention_decode_workspace_bytes(const rpp_kv_cfg* cfg, int n, int nh);
 RPP_API rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* q,
                                         int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,

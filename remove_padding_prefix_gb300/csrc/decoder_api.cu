@@ -10,6 +10,8 @@ namespace {
 // and tiles are rounded up without care.  The same for pages and the kernels' strides over them.
 constexpr long long kMostRows = 0x7fffffffLL - 65535;
 constexpr int kMostPages = 1 << 30;
+// The kernels take scale * log2(e), which has to be finite: 0 scores are NaN otherwise.
+constexpr float kMostScale = 2.0e38f;
 
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -135,7 +137,7 @@ rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache
   if (!q || !out || !workspace || layer < 0 || layer >= cfg->layers || n <= 0 || nh <= 0 || nh % cfg->kv_heads)
     return RPP_EINVAL;
   if (!slots && n > cfg->slots) return RPP_EINVAL;
-  if (!(scale > 0.f) || scale > 3.0e38f) return RPP_EINVAL;
+  if (!(scale > 0.f) || scale > kMostScale) return RPP_EINVAL;
   if (n > kKvMaxList || nh > 65535) return RPP_EUNSUPPORTED;
   if ((cfg->head_dim != 64 && cfg->head_dim != 128) || cfg->page_size % 16) return RPP_EUNSUPPORTED;
   if (!aligned(q, 16) || !aligned(out, 16) || q_stride % 8 ||
@@ -155,7 +157,7 @@ rpp_status rpp_attention_causal_varlen(const void* q, const void* k, const void*
   if (!q || !k || !v || !cu_seqlens || !out || B <= 0 || T_max <= 0 || max_len <= 0 || nh <= 0 || nkv <= 0 ||
       nh % nkv || d <= 0)
     return RPP_EINVAL;
-  if (!(scale > 0.f) || scale > 3.0e38f) return RPP_EINVAL;
+  if (!(scale > 0.f) || scale > kMostScale) return RPP_EINVAL;
   if (dtype != RPP_F16 && dtype != RPP_BF16) return RPP_EUNSUPPORTED;
   if (!attention_causal_supported(B, max_len, d)) return RPP_EUNSUPPORTED;
   if (T_max > kMostRows || (static_cast<long long>(T_max) / 128 + B) * nh > 0x7fffffffLL ||

@@ -143,3 +143,11 @@ def test_causal_arguments(lib, kw, status):
     assert lib.rpp_attention_causal_varlen(g["q"], g["k"], g["v"], g["ldq"], g["ld"], g["cu"], g["B"], g["T"],
                                            g["max_len"], g["nh"], g["nkv"], g["d"], g["dtype"], g["scale"], g["out"],
                                            None, None) == status
+
+
+@pytest.mark.parametrize("scale", [3.0e38, 2.4e38])
+def test_scales_whose_base_2_form_overflows(lib, scale):
+    """The kernels work with scale * log2(e): past the largest float it would make 0 scores NaN."""
+    assert calls(lib, cfg(), cache(), scale=scale)["decode"]() == EINVAL
+    assert lib.rpp_attention_causal_varlen(256, 256, 256, 256, 128, 256, 3, 100, 60, 4, 2, 64, _abi.RPP_BF16, scale, 256,
+                                           None, None) == EINVAL
