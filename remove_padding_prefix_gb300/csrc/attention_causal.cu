@@ -44,9 +44,8 @@
 // the sequence are zeroed in shared memory, and elements of V that are not finite are
 // taken out before the product; the outputs of the rows that see them are written from V once
 // more (their sums with positive weights are the elements themselves), and so are outputs that a weight
-// of 0 times an infinity in an earlier tile made NaN (looking for them: 42.7 against 41.8 us on the short
-// prompts above).  Two warps do that for every V tile
-// before the product may read it, so their wait on a ring slot is never a phase off.  Every mbarrier wait is bounded; a
+// of 0 times an infinity in an earlier tile made NaN.  Two warps look over every V tile before the product may
+// read it, so their wait on a ring slot is never a phase off.  Every mbarrier wait is bounded; a
 // wait that gives up records RPP_DERR_TIMEOUT and the CTA drains, frees tensor memory
 // and exits.
 #include <algorithm>
@@ -237,6 +236,55 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Rewrites outputs from V's elements that are not finite: in a column of row i, one of the 32 rows from `own` on,
+// the sum of those elements in rows 0 .. i, where there is one.  A whole warp, a lane with one of the rows
+// (inv: one over its sum, redo: whether it has to be done; nothing is done where none has to) and with
+// D / 32 columns: it goes through V's rows in order and writes what its rows have by then.  k, v, o: the
+// first row of the sequence, len rows long, in the head's columns.  A call, so that neither its code nor its
+// registers are the kernel's (inlined: 512 prompts of 64 tokens, 32 heads, d = 128, 7% more).
+template <typename T, int D>
+__device__ __noinline__ void sums_of_nonfinite(const T* k, const T* v, int kv_stride, T* o, long long pitch, int own,
+                                               int len, float inv, bool redo) {
+  // rows whose sum is a number: all their scores are, or -inf (elsewhere the whole row is NaN)
+  const bool number = inv > 0.f && inv < __int_as_float(0x7f800000);
+  const uint32_t sound = __ballot_sync(0xffffffffu, number);
+  if (!__any_sync(0xffffffffu, redo && number && own + static_cast<int>(lane_id()) < len)) return;
+  const int end = min(own + 32, len);
+  constexpr int E = D / 32;                      // columns of a lane
+  constexpr int U = 8;                           // rows at a time
+  const int col = lane_id() * E;
+  float sum[E] = {};
+  uint32_t got = 0;                              // columns that have one
+#pragma unroll 1
+  for (int j0 = 0; j0 < end; j0 += U) {          // own is a multiple of U
+    uint32_t w[U][E / 2];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e)
+        w[j][e] = j0 + j < end ? *reinterpret_cast<const uint32_t*>(v + static_cast<long long>(j0 + j) * kv_stride + col + 2 * e) : 0u;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) bad |= ((nonfinite2<T>(w[j][e / 2]) >> (16 * (e & 1) + 15)) & 1u) << e;
+      if (__any_sync(0xffffffffu, bad != 0)) {
+        // a K row that is not finite has the score -inf in a sound row: weight 0, and 0 * inf is NaN
+        const bool none = __any_sync(0xffffffffu, part_nonfinite<T, D>(k + static_cast<long long>(j0 + j) * kv_stride + col));
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((bad >> e) & 1u) sum[e] += none ? __int_as_float(0x7fffffff) : half_of<T>(w[j][e / 2], e & 1);
+        got |= bad;
+      }
+      if (j0 >= own && j0 + j < end && ((sound >> (j0 + j - own)) & 1u)) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((got >> e) & 1u) o[(j0 + j) * pitch + col + e] = from_f32<T>(sum[e]);
+      }
+    }
+  }
 }
 
 template <typename T, int D, bool PAIR>
@@ -729,46 +777,31 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
       }
       ++no;
       tc_fence_after();
-      // O leaves tensor memory whole, so that the next item's first PV can start
-      uint32_t ov[D];
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_ld_32x32b_x32(t_o + 32 * c, ov + 32 * c);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_ld_wait_tied32(ov + 32 * c);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
-      // rows whose sum is a number: all their scores are, or -inf (elsewhere the whole row is NaN)
-      const bool number = l > 0.f && l < __int_as_float(0x7f800000);
-      bool nan_seen = false;                         // outputs that are NaN all the same (one tile: V is looked over)
-      if (nt > 1) {
-        float nan[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < D; e += 2)
-          nan[e / 2 & 3] = max3_nan(nan[e / 2 & 3], __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]));
-        const float one = max3_nan(max3_nan(nan[0], nan[1], nan[2]), nan[3], 0.f);
-        nan_seen = __any_sync(0xffffffffu, number && one != one && it.q0 + quad * 32 + lane < it.len);
-      }
       const float inv = __fdividef(1.0f, l);
       const uint64_t inv2 = f2_pack(inv, inv);
       // A thread has a row, a store wants whole lines: 32 columns at a time through 2 KB of shared
       // memory of the warp's own (16-byte chunk u of row r at u ^ (r / 2 & 3): no bank conflict
-      // either way), then four lanes a row.
+      // either way), then four lanes a row.  Rolled: every instruction here runs once or twice an item, and
+      // fetching it is what that costs.
       const long long pitch = static_cast<long long>(nh) * D;
       const int rr = lane >> 2, ch = lane & 3;         // row of an 8-row group and chunk that this lane stores
       T* obase = out + (it.c0 + it.q0 + quad * 32 + rr) * pitch + it.h * D + 8 * ch;
       const int rows_left = it.len - it.q0 - quad * 32 - rr;
-#pragma unroll
+      uint64_t all2[2] = {0ull, 0ull};                 // sum of the row's outputs
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld_32x32b_x32(t_o + 32 * c, x);
+        tmem_ld_wait_tied32(x);
         uint8_t* mine = stage + lane * 64;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(ov[32 * c + 8 * u + 2 * e]),
-                                               __uint_as_float(ov[32 * c + 8 * u + 2 * e + 1])), inv2);
+            const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(x[8 * u + 2 * e]), __uint_as_float(x[8 * u + 2 * e + 1])), inv2);
             w[e] = pack2<T>(f2_lo(x2), f2_hi(x2));
+            all2[e & 1] = f2_add(all2[e & 1], x2);
           }
           *reinterpret_cast<uint4*>(mine + ((u ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -781,49 +814,19 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
         }
         __syncwarp();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
       // V elements that are not finite: a column that has one up to a row's own key is there the sum of such
-      // elements, which needs neither weights nor the finite rest.  They were taken out of the diagonal tile,
-      // and before it a weight that underflowed to 0 made NaN of one (nonfinite.cuh).  Where that
-      // happened the warp goes through V's rows in order, a lane with D / 32 columns, and writes what its rows
-      // have by then.  (The note is visible here: o_full came after the v_ready of that tile.)
-      if (live && (nan_seen || met[(r - 1) & 7] == r)) {
-        constexpr int E = D / 32;                      // columns of a lane
-        constexpr int U = D / 16;                      // rows at a time: twice as many would spill
-        const long long first = static_cast<long long>(it.c0) * kv_stride + it.h / group * D + lane * E;
-        const T *kr = k_rows + first, *vr = v_rows + first;
-        T* o = out + static_cast<long long>(it.c0) * pitch + it.h * D + lane * E;
-        const int own = it.q0 + quad * 32, end = min(own + 32, it.len);
-        const uint32_t sound = __ballot_sync(0xffffffffu, number);
-        float sum[E] = {};
-        uint32_t got = 0;                              // columns that have one
-#pragma unroll 1
-        for (int k0 = 0; k0 < end; k0 += U) {          // own is a multiple of U
-          uint32_t w[U][E / 2];
-#pragma unroll
-          for (int k = 0; k < U; ++k)
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-              w[k][e] = k0 + k < end ? *reinterpret_cast<const uint32_t*>(vr + static_cast<long long>(k0 + k) * kv_stride + 2 * e) : 0u;
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            uint32_t bad = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) bad |= ((nonfinite2<T>(w[k][e / 2]) >> (16 * (e & 1) + 15)) & 1u) << e;
-            if (__any_sync(0xffffffffu, bad != 0)) {
-              // a K row that is not finite has the score -inf in a sound row: weight 0, and 0 * inf is NaN
-              const bool none = __any_sync(0xffffffffu, part_nonfinite<T, D>(kr + static_cast<long long>(k0 + k) * kv_stride));
-#pragma unroll
-              for (int e = 0; e < E; ++e)
-                if ((bad >> e) & 1u) sum[e] += none ? __int_as_float(0x7fffffff) : half_of<T>(w[k][e / 2], e & 1);
-              got |= bad;
-            }
-            if (k0 >= own && k0 + k < end && ((sound >> (k0 + k - own)) & 1u)) {
-#pragma unroll
-              for (int e = 0; e < E; ++e)
-                if ((got >> e) & 1u) o[(k0 + k) * pitch + e] = from_f32<T>(sum[e]);
-            }
-          }
-        }
+      // elements, which needs neither weights nor the finite rest.  They were taken out of the diagonal tile (the
+      // note is visible here: o_full came after the v_ready of that tile), and before it a weight that underflowed
+      // to 0 made NaN of one (nonfinite.cuh), which the sum of the row's outputs shows.
+      const float all = (f2_lo(all2[0]) + f2_hi(all2[0])) + (f2_lo(all2[1]) + f2_hi(all2[1]));
+      const bool noted = met[(r - 1) & 7] == r, nan = all != all;
+      if (live && (noted || (nt > 1 && __any_sync(0xffffffffu, nan)))) {
+        const long long first = static_cast<long long>(it.c0) * kv_stride + it.h / group * D;
+        sums_of_nonfinite<T, D>(k_rows + first, v_rows + first, kv_stride, out + static_cast<long long>(it.c0) * pitch + it.h * D,
+                                pitch, it.q0 + quad * 32, it.len, inv, noted || nan);
       }
     }
     if (!ok && lane == 0) {

@@ -382,3 +382,28 @@ def test_a_value_that_is_not_finite_costs_its_own_rows_only():
     spoilt = best()
     assert (out[0:lens[0], 3] == float("inf")).all()
     assert spoilt <= 2 * plain, (spoilt, plain)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nh", [1, 2])
+def test_rows_whose_scores_are_no_numbers_stay_nan(d, nh):
+    """A query that holds NaN, or one whose scores are all -inf, beside values that are not finite: its row is NaN, the
+    rows around it have the infinity."""
+    lens = [400, 60]
+    q, k, v = make(lens, nh, 1, d, "bf16")
+    k[:, 0] = k[:, 0].abs() + 0.5
+    q[200, :] = float("nan")
+    q[310, :] = 0
+    q[310, ::d] = float("-inf")
+    v[3, 5] = float("inf")
+    v[305, 6] = float("-inf")
+    out = rpp.attention_causal_varlen(q, k, v, ints(cu_of(lens)), 2, 400, nh, 1, d)
+    nans = torch.isnan(out.float())
+    assert nans[200].all() and nans[310].all()
+    rest = [i for i in range(460) if i not in (200, 310)]
+    assert not nans[rest].any()
+    for h in range(nh):
+        col = out[:400, h * d + 5].float()
+        assert (col[[i for i in rest if 3 <= i < 400]] == float("inf")).all() and torch.isfinite(col[:3]).all()
+        col = out[:400, h * d + 6].float()
+        assert (col[[i for i in rest if 305 <= i < 400]] == float("-inf")).all() and torch.isfinite(col[:200]).all()

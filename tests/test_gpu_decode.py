@@ -348,3 +348,18 @@ def test_an_infinite_value_of_a_small_weight(dtype, far, rows, first):
     put(c, 0, 0, at, 0, 0, float("-inf"))
     got = rpp.attention_decode(c, 0, q, slots)
     assert torch.isnan(got[:, 7:10]).all() and torch.isfinite(got[:, 10:].float()).all()
+
+
+def test_rows_whose_scores_are_no_numbers_stay_nan():
+    """A query head that holds NaN beside an infinite value: NaN all over, the other heads have the infinity."""
+    c = make("fp16", [700, 90], 1, 64, 16)
+    q = queries(2, 5, 64, "fp16").clone()
+    q[:, 64 * 3 + 7] = float("nan")
+    for s in (0, 1):
+        put(c, 1, s, 30, 0, 5, float("inf"))
+    out = rpp.attention_decode(c, 0, q).float().view(2, 5, 64)
+    assert torch.isnan(out[:, 3]).all()
+    rest = out[:, [0, 1, 2, 4]]
+    assert (rest[..., 5] == float("inf")).all()
+    keep = [e for e in range(64) if e != 5]
+    assert torch.isfinite(rest[..., keep]).all()
