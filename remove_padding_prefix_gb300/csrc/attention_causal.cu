@@ -5,8 +5,8 @@
 //
 // A work item is (sequence, query head, tile of 128 queries), run against 128-key tiles of K and
 // V, the diagonal tile last.  A stream of items is 256 threads and half of tensor memory; an SM has two,
-// so that while one's softmax runs the tensor cores have the other's products.  Where a kv head
-// has an even number of query heads, the two are one CTA's and take the two heads of a pair over
+// so that while one's softmax runs the tensor cores have the other's products.  At d = 128, where a
+// kv head has an even number of query heads, the two are one CTA's and take the two heads of a pair over
 // one ring of K and V tiles: a tile then costs one write into shared memory for two products.
 // Shared memory is the narrowest place at d = 128: S reads 64 KB a tile, PV 32 KB, and the
 // tile itself is 64 KB, 1280 cycles of 128 bytes in all against 1024 of the tensor cores; 1024
@@ -65,7 +65,7 @@ constexpr int kT = 128;                  // queries of an item, keys of a tile
 constexpr int kMaxPrompts = 4096;        // sequences of a call (their bounds are held in shared memory)
 constexpr int kMaxCausalLen = 262144;    // tokens of a sequence (its tile counts are held there too)
 
-// PAIR: a CTA runs two streams of items side by side, the heads 2 i and 2 i + 1 of one kv head, over one ring
+// PAIR (d = 128 only): a CTA runs two streams of items side by side, the heads 2 i and 2 i + 1 of one kv head, over one ring
 // of K and V tiles; else one stream, and two CTAs an SM.  A stream has 256 threads and 256 columns of
 // tensor memory either way.
 template <int D, bool PAIR>
@@ -871,13 +871,12 @@ cudaError_t launch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t dispatch(const Maps& t, const CausalArgs& a, cudaStream_t stream) {
-  // Pairs of heads wherever a kv head has an even number of them.  Pairs against single streams, 32 heads on
-  // 8 kv heads, d = 128: 674 / 789 us for two prompts of 8192 and 7500, 286 / 317 us for 32 of 1024, 132 / 129
-  // us for 256 of 128, 192 / 219 us for 512 of 64; 16 heads on 4, d = 64: 340 / 357 us for 8 of 4096,
-  // 61 / 61 us for 256 of 128.
-  const bool pair = (a.nh / a.nkv) % 2 == 0;
-  if (a.d == 64) return pair ? launch<T, 64, true>(t, a, stream) : launch<T, 64, false>(t, a, stream);
-  return pair ? launch<T, 128, true>(t, a, stream) : launch<T, 128, false>(t, a, stream);
+  // Pairs of heads at d = 128, where a kv head has an even number of them.  Pairs against single streams, 32 heads
+  // on 8 kv heads, d = 128: 621 / 740 us for two prompts of 8192 and 7500, 292 / 314 us for 32 of 1024, 142 / 129
+  // us for 256 of 128, 210 / 217 us for 512 of 64.  At d = 64 shared memory is not the narrowest place: 16
+  // heads on 4, 350 / 341 us for 8 of 4096, 61 / 60 us for 256 of 128.
+  if (a.d == 64) return launch<T, 64, false>(t, a, stream);
+  return (a.nh / a.nkv) % 2 == 0 ? launch<T, 128, true>(t, a, stream) : launch<T, 128, false>(t, a, stream);
 }
 
 }  // namespace
