@@ -548,6 +548,9 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
  * k and v of kv head h / (nh / nkv).  Rows that a query must not see have no effect on
  * it, whatever they hold (infinities and NaN among it); a value that it sees and that is not finite
  * gives what the formula does, a weight being above 0, however small, but for a score of -inf.
+ * The weights are rounded to dtype for their product with v (their sum is not), off by up to 2^-8 (bf16)
+ * or 2^-11 (fp16) of each; sums are fp32 before the division, of weights up to 2^8: bf16 values above
+ * 2^100 may overflow them.
  *  q       device rows of nh * d of dtype, q_stride elements apart; k, v: rows of nkv * d,
  *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
  *          QKV projection's output); T_max <= 2^31 - 65536 rows each
@@ -564,6 +567,7 @@ RPP_API rpp_status rpp_attention_causal_varlen(const void* q, const void* k, con
  * K and V of kv head h / (nh / kv_heads).  The new token's own K and V are in the cache
  * (reserve, append) before the call; a sequence of length 0 gives zeros.  A value that is not
  * finite gives what the formula does: a weight is above 0, however small, but for a score of -inf.
+ * Sums are fp32 before the division, of weights up to 2^8 (bf16 values above 2^88 may overflow them).
  *  q      device rows of nh * head_dim of dtype, q_stride elements apart (a multiple of 8)
  *  slots  device int32[n], NULL: slots 0 .. n-1; a slot may be named several times
  *  out    device [n, nh * head_dim] of dtype; must not overlap q.  After a device error

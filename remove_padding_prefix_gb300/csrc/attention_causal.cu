@@ -26,15 +26,23 @@
 //               tile goes block by block, those of 32 keys that none of a warp's queries sees are
 //               passed over.  At the end O / sum goes to the output row.
 //
-// Measured (bf16, one GB300): 8192 and 7500 tokens, 32 heads on 8 kv heads, d = 128: 674 us, 1500
-// TFLOP/s, 0.80 of the measured cuBLAS burst; first version 891 us, with streams as CTAs of their
-// own 789.  64 prompts of 32 to 384, 16 heads, d = 64: 43 us against 16 us of reading and
-// writing once: a softmax warp's item is some 1500 instructions that wait for one another, and
-// tensor memory has room for two such chains an SM; four, with 64-key tiles, took as long.
+// Measured (bf16, one GB300): 8192 and 7 thousand tokens, 32 heads on 8 kv heads, d = 128: 720 us, 1480
+// TFLOP/s, 0.79 of the measured cuBLAS burst.  64 prompts of 32 to 384, 16 heads, d = 64: 41.5 us against 16 us
+// of reading and writing once: a softmax warp's item is some 1500 instructions that wait for one another, and
+// tensor memory has room for two such chains an SM; four, with 64-key tiles, took as long.  8 prompts of
+// 4096, 16 heads, d = 64: 351 us, 0.42 of the burst, by the same chain: a tile is half the products of d = 128
+// for as many weights (tensor pipe 32%, exponentials 31%, issue slots 46% over one such prompt).
+//
+// P goes into its product in the type of the inputs, as the tensor cores take it: off by up to half a step of
+// each weight (2^-8 of it in bf16, 2^-11 in fp16), as in the library's other attention.  A second product
+// for what the rounding left, as in attention_decode.cu, would be half as many products again, and they
+// bound long prompts.  The sum of the weights is of the unrounded ones.
 //
 // Items are taken longest first: with causal masking the cost of a query tile is its place
 // in its sequence, so the list is by falling place, all sequences long enough and all
 // heads at each (the heads of a kv head side by side: their K and V come from L2).
+// One thread goes through the ceil(max_len / 128) places, so a max_len far above the lengths costs time: the
+// 64 prompts above 86 us with 131072 and 140 with 262144, where the list is also too large for two single streams an SM.
 // Every CTA builds the same list from cu_seqlens in its prologue and walks it there and back
 // (item r CTAs + c in even rounds, r CTAs + CTAs - 1 - c in odd ones), which evens out the fall
 // of the costs without a counter in memory.
@@ -88,7 +96,8 @@ struct Shape {
   static constexpr uint32_t kOffList = kOffMisc + 64;
 };
 // Registers: launched with 128 a thread, 32768 a stream (checked at the first launch: a split above
-// what the launch has would wait for ever); 128 threads keep 80, the softmax's 128 take 176.
+// what the launch has would wait for ever); 128 threads keep 80, the softmax's 128 take 176.  The compiler
+// spills 20 to 48 bytes a thread in all.
 constexpr int kLaunchRegs = 128, kLowRegs = 80, kHighRegs = 176;
 static_assert(kLowRegs + kHighRegs == 2 * kLaunchRegs, "the split must be the launch's registers");
 

@@ -609,7 +609,7 @@ cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* fro
                            int32_t* err, cudaStream_t stream) {
   // More CTAs than fit at once: the pairs' last pages are full to different degrees, and a share of
   // an empty one costs a CTA's start only.  16 prompts forked 8 times over 12 layers, with the free
-  // before it: 71 us at 8 CTAs an SM, 64 at 32, 71 at 64, 87 at 128.
+  // before it: 73 us at 8 CTAs an SM, 66.6 at 16, 66.4 at 32, 75 at 64, 93 at 128; 4 forked twice 13.6 at each.
   const long long vec = static_cast<long long>(d.layers) * 2 * d.kv_heads * (d.page_size - 1) * (d.head_dim / 8);
   const int x = blocks_for(n, 32 * num_sms());
   const int most = (32 * num_sms() + x - 1) / x;
