@@ -293,6 +293,11 @@ __device__ __noinline__ void sums_of_nonfinite(const T* k, const T* v, int kv_st
           if ((got >> e) & 1u) o[(j0 + j) * pitch + col + e] = from_f32<T>(sum[e]);
       }
     }
+    // nothing changes a NaN any more: on to the warp's own rows (a sequence whose values are NaN all over)
+    bool fixed = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) fixed = fixed && sum[e] != sum[e];
+    if (j0 < own && __all_sync(0xffffffffu, fixed)) j0 = own - U;
   }
 }
 

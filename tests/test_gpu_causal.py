@@ -407,3 +407,19 @@ def test_rows_whose_scores_are_no_numbers_stay_nan(d, nh):
         assert (col[[i for i in rest if 3 <= i < 400]] == float("inf")).all() and torch.isfinite(col[:3]).all()
         col = out[:400, h * d + 6].float()
         assert (col[[i for i in rest if 305 <= i < 400]] == float("-inf")).all() and torch.isfinite(col[:200]).all()
+
+
+@pytest.mark.parametrize("d,nh,nkv", [(64, 2, 2), (128, 4, 2), (128, 3, 3)])
+def test_values_that_are_nan_all_over(d, nh, nkv):
+    """Every item of a long prompt takes its outputs from the values: no wait runs out meanwhile, and the prompts
+    beside it are as without it."""
+    lens = [200, 20000, 333]
+    q, k, v = make(lens, nh, nkv, d, "bf16")
+    a = (ints(cu_of(lens)), 3, 20000, nh, nkv, d)
+    base = rpp.attention_causal_varlen(q, k, v, *a)
+    v[200:20200] = float("nan")
+    err = rpp.new_error_word()
+    out = rpp.attention_causal_varlen(q, k, v, *a, err=err)
+    assert rpp.get_device_error(err) == 0
+    assert torch.isnan(out[200:20200]).all()
+    assert torch.equal(out[:200], base[:200]) and torch.equal(out[20200:], base[20200:])

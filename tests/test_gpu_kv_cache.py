@@ -469,3 +469,11 @@ def test_append_with_a_step_back_far_down_the_list():
     cu[700] -= 2
     rpp.kv_append(p.gpu, 0, k, v, ints(list(range(n))), ints(cu))
     p.check(od.LENGTH)
+
+
+def test_fork_of_an_empty_sequence():
+    p = _some()
+    p.fork([3, 0, 3], [2, 4, 5])
+    p.check()
+    p.grow([2, 5], [17, 3])
+    p.check()
