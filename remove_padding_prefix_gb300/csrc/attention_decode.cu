@@ -456,32 +456,64 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
         redo = redo || (sound[e] && nan != nan);
       }
       if (__any_sync(0xffffffffu, redo)) {
-        // The unit's keys in this share once more, V's elements that are not finite into the outputs.  A K row
-        // that is not finite has the score -inf in a sound row: weight 0, and 0 * inf is NaN.
+        // The unit's keys in this share once more, eight at a time (of one page), a lane with E columns: the sum of
+        // V's elements that are not finite is the output of every row that is sound.  A K row that is not finite
+        // has the score -inf in such a row: weight 0, and 0 * inf is NaN.
+        constexpr int E = D / 32;
         const int here = static_cast<int>(f - f0 < cc.blk ? f - f0 : cc.blk) + 1;
         const int k1 = min(cc.len, (cc.blk + 1) * KB);
+        float sum[E] = {};
         uint32_t got = 0;           // columns that have one
+        int next = __ldg(cc.row + (cc.blk + 1 - here) * KB / ps);
 #pragma unroll 1
-        for (int key = (cc.blk + 1 - here) * KB; key < k1; ++key) {
-          const int pg = __ldg(cc.row + key / ps);
+        for (int key = (cc.blk + 1 - here) * KB; key < k1; key += 8) {
+          const int pg = next;      // read while the rows before were under way
+          if (key + 8 < k1) next = __ldg(cc.row + (key + 8) / ps);
           if (pg < 0 || pg >= p.d.pages) continue;
-          const T* kr = pool + pg * page_elems + head * head_elems + static_cast<long long>(key % ps) * D;
+          const T* kr = pool + pg * page_elems + head * head_elems + static_cast<long long>(key % ps) * D + lane * E;
           const T* vr = kr + v_off;
-          if (!__any_sync(0xffffffffu, part_nonfinite<T, D>(vr + lane * (D / 32)))) continue;
-          const bool none = __any_sync(0xffffffffu, part_nonfinite<T, D>(kr + lane * (D / 32)));
+          uint32_t w[8][E / 2], bad = 0, none = 0;     // none: rows of weight 0
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(vr + 8 * j + 2 * t);
-            const uint32_t bad = nonfinite2<T>(w);
+          for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (!((bad >> (16 * c + 15)) & 1u)) continue;
-              const float x = none ? __int_as_float(0x7fffffff) : half_of<T>(w, c);
+            for (int e = 0; e < E / 2; ++e)
+              w[j][e] = key + j < k1 ? *reinterpret_cast<const uint32_t*>(vr + j * D + 2 * e) : 0u;
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (sound[e]) o[j][2 * e + c] = ((got >> (2 * j + c)) & 1u ? o[j][2 * e + c] : 0.f) + x;
-              got |= 1u << (2 * j + c);
+          for (int j = 0; j < 8; ++j)
+            if (key + j < k1 && part_nonfinite<T, D>(kr + j * D)) none |= 1u << j;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) bad |= nonfinite2<T>(w[j][e]);
+          if (!__any_sync(0xffffffffu, (bad & 0x80008000u) != 0)) continue;
+          none = __reduce_or_sync(0xffffffffu, none);
+          bool fixed = true;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (!((nonfinite2<T>(w[j][e / 2]) >> (16 * (e & 1) + 15)) & 1u)) continue;
+              sum[e] += (none >> j) & 1u ? __int_as_float(0x7fffffff) : half_of<T>(w[j][e / 2], e & 1);
+              got |= 1u << e;
             }
+            fixed = fixed && sum[e] != sum[e];
+          }
+          if (__all_sync(0xffffffffu, fixed)) break;   // NaN in all columns stays
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          const int from = (8 * j + 2 * t) / E;        // the lane with this one's two columns, and which of its own they are
+          const uint32_t theirs = __shfl_sync(0xffffffffu, got, from) >> (2 * t & (E - 1));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = __shfl_sync(0xffffffffu, sum[c], from);
+            if constexpr (E == 4) {
+              const float y = __shfl_sync(0xffffffffu, sum[2 + c], from);
+              if (t & 1) x = y;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (sound[e] && ((theirs >> c) & 1u)) o[j][2 * e + c] = x;
           }
         }
       }
