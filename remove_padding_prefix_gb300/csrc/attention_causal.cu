@@ -247,19 +247,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Rewrites outputs from V's elements that are not finite: in a column of row i, one of the 32 rows from `own` on,
-// the sum of those elements in rows 0 .. i, where there is one.  A whole warp, a lane with one of the rows
-// (inv: one over its sum, redo: whether it has to be done; nothing is done where none has to) and with
-// D / 32 columns: it goes through V's rows in order and writes what its rows have by then.  k, v, o: the
-// first row of the sequence, len rows long, in the head's columns.  A call, so that neither its code nor its
-// registers are the kernel's (inlined: 512 prompts of 64 tokens, 32 heads, d = 128, 7% more).
+// Rewrites outputs from V's elements that are not finite, of the 32 rows from `own` on.  A whole warp, a lane with one
+// of the rows (inv: one over its sum, nan: whether its output held NaN) and with D / 32 columns: it goes through V's
+// rows in order, and a row's output in a column that has had such elements by then is their sum.  Where no
+// sound row held NaN the tiles before the diagonal are in the outputs already, and the sum is of the diagonal tile's
+// (noted: it has some) and added.  k, v, o: the first row of the sequence, len rows long, in the head's columns.
+// A call, so that neither its code nor its registers are the kernel's (inlined: 512 prompts of 64 tokens, 32
+// heads, d = 128, 7% more).
 template <typename T, int D>
 __device__ __noinline__ void sums_of_nonfinite(const T* k, const T* v, int kv_stride, T* o, long long pitch, int own,
-                                               int len, float inv, bool redo) {
+                                               int len, float inv, bool nan, bool noted) {
   // rows whose sum is a number: all their scores are, or -inf (elsewhere the whole row is NaN)
-  const bool number = inv > 0.f && inv < __int_as_float(0x7f800000);
+  const bool number = inv > 0.f && inv < __int_as_float(0x7f800000) && own + static_cast<int>(lane_id()) < len;
   const uint32_t sound = __ballot_sync(0xffffffffu, number);
-  if (!__any_sync(0xffffffffu, redo && number && own + static_cast<int>(lane_id()) < len)) return;
+  const bool whole = __any_sync(0xffffffffu, nan && number);
+  if (!whole && (!noted || !sound)) return;
   const int end = min(own + 32, len);
   constexpr int E = D / 32;                      // columns of a lane
   constexpr int U = 8;                           // rows at a time
@@ -267,7 +269,7 @@ __device__ __noinline__ void sums_of_nonfinite(const T* k, const T* v, int kv_st
   float sum[E] = {};
   uint32_t got = 0;                              // columns that have one
 #pragma unroll 1
-  for (int j0 = 0; j0 < end; j0 += U) {          // own is a multiple of U
+  for (int j0 = whole ? 0 : own / kT * kT; j0 < end; j0 += U) {   // own is a multiple of U
     uint32_t w[U][E / 2];
 #pragma unroll
     for (int j = 0; j < U; ++j)
@@ -290,7 +292,10 @@ __device__ __noinline__ void sums_of_nonfinite(const T* k, const T* v, int kv_st
       if (j0 >= own && j0 + j < end && ((sound >> (j0 + j - own)) & 1u)) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if ((got >> e) & 1u) o[(j0 + j) * pitch + col + e] = from_f32<T>(sum[e]);
+          if ((got >> e) & 1u) {
+            T* at = o + (j0 + j) * pitch + col + e;
+            *at = from_f32<T>(whole ? sum[e] : sum[e] + to_f32(*at));
+          }
       }
     }
     // nothing changes a NaN any more: on to the warp's own rows (a sequence whose values are NaN all over)
@@ -840,7 +845,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
       if (live && (noted || (nt > 1 && __any_sync(0xffffffffu, nan)))) {
         const long long first = static_cast<long long>(it.c0) * kv_stride + it.h / group * D;
         sums_of_nonfinite<T, D>(k_rows + first, v_rows + first, kv_stride, out + static_cast<long long>(it.c0) * pitch + it.h * D,
-                                pitch, it.q0 + quad * 32, it.len, inv, noted || nan);
+                                pitch, it.q0 + quad * 32, it.len, inv, nan, noted);
       }
     }
     if (!ok && lane == 0) {

@@ -423,3 +423,21 @@ def test_values_that_are_nan_all_over(d, nh, nkv):
     assert rpp.get_device_error(err) == 0
     assert torch.isnan(out[200:20200]).all()
     assert torch.equal(out[:200], base[:200]) and torch.equal(out[20200:], base[20200:])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,nh", [(64, 2), (128, 1), (128, 2)])
+def test_infinities_before_and_in_the_diagonal_tile(d, nh, dtype):
+    """A row's output in a column is the sum of the infinities up to it, in whichever tiles they lie; other columns are as
+    without them."""
+    lens, inf = [500, 300], float("inf")
+    q, k, v = make(lens, nh, 1, d, dtype, seed=4, qscale=0.5)
+    a = (ints(cu_of(lens)), 2, 500, nh, 1, d)
+    want = rpp.attention_causal_varlen(q, k, v, *a).clone()
+    for row, col, x in ((5, 3, inf), (390, 3, -inf), (200, 4, -inf), (450, 4, -inf), (128, 5, inf), (499, 6, float("nan"))):
+        v[row, col] = x
+    for h in range(nh):
+        w = want[:500, h * d:(h + 1) * d]
+        w[5:, 3], w[390:, 3], w[200:, 4], w[128:, 5], w[499:, 6] = inf, float("nan"), -inf, inf, float("nan")
+    got = rpp.attention_causal_varlen(q, k, v, *a)
+    assert ((got == want) | (torch.isnan(got) & torch.isnan(want))).all()
