@@ -465,7 +465,8 @@ RPP_API rpp_status rpp_patch_merge_forward(const rpp_merge_cfg* cfg, const void*
  *   refs   int32[pages], 16-byte aligned: sequences that use the page; 0 = free.  Zero at the start.
  * A slot uses the first ceil(lens / page_size) entries of its table row; the others are
  * never read.  Free pages are taken lowest number first, in the order of the call's list:
- * the state after a call depends on the state before it and nothing else.
+ * the state after a call depends on the state before it and nothing else (but for what an append or
+ * a free leaves out after an error, below).
  *
  * Lists of slots are device int32[n], 1 <= n <= 4096.  `err` is required by the calls that change
  * a cache.  A slot out of range, or given twice to reserve, append, fork (destinations) or free,

@@ -6,7 +6,8 @@
 // a page).  A page is free where refs is 0; pages are taken lowest number first, in the
 // order of the call's list, so every result is a function of the state alone: there is
 // no free list whose order could depend on history, and no atomic whose order shows
-// (reference counts are only added to).
+// (reference counts are only added to).  What an append or a free leaves out after an error of its own
+// does depend on timing: their CTAs read the error word as they start.
 //
 // The kernels that decide (who gets which page, what moves where) are one CTA each: they
 // read refs, 4 bytes a page, twice, against 2 * kv heads * rows * head size * 2 bytes a
