@@ -58,7 +58,7 @@ typedef enum rpp_status {
   RPP_EDEVICE = -5        /* rpp_get_device_error found a nonzero device error word */
 } rpp_status;
 
-typedef enum rpp_dtype { RPP_F32 = 0, RPP_F16 = 1, RPP_BF16 = 2, RPP_I8 = 3 } rpp_dtype;
+typedef enum rpp_dtype { RPP_F32 = 0, RPP_F16 = 1, RPP_BF16 = 2, RPP_I8 = 3, RPP_E4M3 = 4 } rpp_dtype;
 
 /* codes written into the device error word */
 #define RPP_DERR_LENGTH 1   /* a sequence length outside [0, L] or [0, max_len] */
@@ -543,6 +543,20 @@ RPP_API rpp_status rpp_kv_compact(const rpp_kv_cfg* cfg, const rpp_kv_cache* cac
                                   int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
                                   size_t workspace_bytes, int32_t* err, rpp_stream stream);
 
+/* Reads rows of n sequences back from one layer, as rpp_kv_append takes them.
+ *  slots       device int32[n]; a slot may be named several times
+ *  starts      device int32[n]: rows cu[i] .. cu[i+1]-1 receive positions starts[i], starts[i] + 1, ...; NULL: the last
+ *              cu[i+1] - cu[i] tokens of slots[i]
+ *  cu_seqlens  device int32[n+1]; NULL: one row each (rows_max >= n)
+ *  k, v        device rows of kv_heads * head_dim of the cache's dtype, row_stride elements apart; rows from cu[n]
+ *              on are left as they were.  May not overlap the cache
+ * A slot out of range (RPP_DERR_SLOT), cu[i + 1] < cu[i] (RPP_DERR_LENGTH), cu[n] > rows_max or cu[0] < 0
+ * (RPP_DERR_ROWS): nothing is written.  A row of a position that the sequence does not have (RPP_DERR_LENGTH) or on a
+ * page that the pool does not (RPP_DERR_PAGE) is left as it was, and so may others be. */
+RPP_API rpp_status rpp_kv_read(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const int32_t* slots,
+                               const int32_t* starts, const int32_t* cu_seqlens, int n, int rows_max, void* k, void* v,
+                               int row_stride, int32_t* err, rpp_stream stream);
+
 /* Causal attention over packed prompts of different lengths, grouped heads: for row i of
  * sequence b (rows cu[b] .. cu[b+1]-1) and head h
  *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j]) v[j],  cu[b] <= j <= i,
@@ -581,6 +595,71 @@ RPP_API size_t rpp_attention_decode_workspace_bytes(const rpp_kv_cfg* cfg, int n
 RPP_API rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache, int layer, const void* q,
                                         int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,
                                         void* workspace, size_t workspace_bytes, int32_t* err, rpp_stream stream);
+
+/* ------------------------------------------------------------------------------
+ * The same cache held in 8 bits: half the bytes of the pool, and of the attention over it.
+ *
+ * The state is the 16-bit cache's but for the pool, int8 or e4m3 codes in the same layout, and one more array:
+ *   scales  uint8[layers, pages, 2, kv_heads, page_size / block], 16-byte aligned; needs no initial contents
+ * `block` tokens of a head share a scale byte b: a code c stands for c * 2^(b - 127), and b = 255 for NaN.  For the
+ * rows that rpp_kv8_append brings to a block, with a the largest magnitude among them,
+ *   b = the smallest byte at which a is no more than half a step past the largest code (127 or 448), or the block's
+ *       own, if it has rows already and that is larger;
+ *   code = x * 2^(127 - b), rounded half to even, saturated.
+ * Where b grew, the codes that the block has are rounded again: as scales are powers of two, everything that a value
+ * loses over the life of its block stays below one step of the block's last scale in int8 (2^(b - 127); half of it if
+ * the block is written at once), and in e4m3 below 2^-4 of the value and 2^-9 2^(b - 127) together.  A value that is
+ * not finite makes its block NaN, all rows and columns of it, until the block's first row is written anew.  A block's rows
+ * are written in order: where an append passes over one (reserved, never written), the block keeps whatever
+ * scale was there before if that is larger.
+ *
+ * Calls, lists, errors and conventions are those of the 16-bit cache.
+ * ------------------------------------------------------------------------------ */
+typedef struct rpp_kv8_cfg {
+  rpp_kv_cfg kv; /* dtype RPP_I8 or RPP_E4M3; head_dim 64 or 128, page_size a multiple of 16 */
+  int block;     /* tokens that share a scale: 1, 2, 4, .. 128, a divisor of page_size */
+} rpp_kv8_cfg;
+
+typedef struct rpp_kv8_cache { /* device pointers */
+  rpp_kv_cache kv;
+  uint8_t* scales;
+} rpp_kv8_cache;
+
+/* Bytes of the pool and of the scales; 0 for a configuration that is not valid or not supported. */
+RPP_API size_t rpp_kv8_pool_bytes(const rpp_kv8_cfg* cfg);
+RPP_API size_t rpp_kv8_scales_bytes(const rpp_kv8_cfg* cfg);
+
+/* As rpp_kv_reserve, _fork, _free and _compact (scales go with their rows and pages). */
+RPP_API rpp_status rpp_kv8_reserve(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, const int32_t* slots,
+                                   const int32_t* counts, int n, int32_t* err, rpp_stream stream);
+RPP_API rpp_status rpp_kv8_fork(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, const int32_t* from,
+                                const int32_t* to, int n, int32_t* err, rpp_stream stream);
+RPP_API rpp_status rpp_kv8_free(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, const int32_t* slots, int n,
+                                int32_t* err, rpp_stream stream);
+RPP_API size_t rpp_kv8_compact_workspace_bytes(const rpp_kv8_cfg* cfg);
+RPP_API rpp_status rpp_kv8_compact(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, int32_t* table_out,
+                                   int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
+                                   size_t workspace_bytes, int32_t* err, rpp_stream stream);
+
+/* As rpp_kv_append, the rows (of dtype, RPP_F16 or RPP_BF16) turned into codes. */
+RPP_API rpp_status rpp_kv8_append(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, int layer, const void* k,
+                                  const void* v, rpp_dtype dtype, int row_stride, const int32_t* slots,
+                                  const int32_t* cu_seqlens, int n, int rows_max, int32_t* err, rpp_stream stream);
+
+/* As rpp_kv_read: each value code * 2^(b - 127), rounded to dtype (RPP_F16 or RPP_BF16; exact in bf16 but for
+ * its smallest values) and saturated to its largest finite value; NaN where b is 255. */
+RPP_API rpp_status rpp_kv8_read(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, int layer, const int32_t* slots,
+                                const int32_t* starts, const int32_t* cu_seqlens, int n, int rows_max, void* k, void* v,
+                                rpp_dtype dtype, int row_stride, int32_t* err, rpp_stream stream);
+
+/* As rpp_attention_decode, over the values code * 2^(b - 127); q and out of dtype, RPP_F16 or RPP_BF16.  Every head
+ * that sees a block of NaN is NaN.  Weights are rounded to two f16 parts for their product with the codes
+ * (together off by up to 2^-22 of each, and 2^-40 of the largest value's scale). */
+RPP_API size_t rpp_attention_decode8_workspace_bytes(const rpp_kv8_cfg* cfg, int n, int nh);
+RPP_API rpp_status rpp_attention_decode8(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, int layer, const void* q,
+                                         rpp_dtype dtype, int q_stride, const int32_t* slots, int n, int nh, float scale,
+                                         void* out, void* workspace, size_t workspace_bytes, int32_t* err,
+                                         rpp_stream stream);
 
 #ifdef __cplusplus
 }

@@ -16,10 +16,10 @@ import numpy as np
 import torch
 
 from . import _abi
-from ._abi import (RPP_F32, RPP_F16, RPP_BF16, RPP_I8, RPP_EPI_BIAS, RPP_EPI_BIAS_GELU,  # noqa: F401
+from ._abi import (RPP_F32, RPP_F16, RPP_BF16, RPP_I8, RPP_E4M3, RPP_EPI_BIAS, RPP_EPI_BIAS_GELU,  # noqa: F401
                    RPP_EPI_BIAS_RESIDUAL, RPP_DERR_LENGTH, RPP_DERR_TIMEOUT, RPP_DERR_ROWS, RPP_DERR_TMEM,
                    RPP_DERR_SLOT, RPP_DERR_PAGE, RPP_DERR_FULL, EncoderCfg, LayerSrc, SwinCfg, SwinSrc, MergeCfg, KvCfg,
-                   KvArrays)
+                   KvArrays, Kv8Cfg, Kv8Arrays)
 
 __all__ = [
     "RppError", "lib", "torch_dtype", "dtype_code", "build_offsets", "remove_padding", "rebuild_padding", "linear",
@@ -27,7 +27,7 @@ __all__ = [
     "encoder_layer_calibrate", "encoder_forward", "quantize_weight", "quantize_activation", "gemm_i8_i32",
     "swin_cfg", "SwinBlock", "swin_prepare_bias", "window_attention_forward", "swin_block_forward",
     "merge_cfg", "PatchMerge", "patch_merge_forward",
-    "KvCache", "kv_reserve", "kv_append", "kv_fork", "kv_free", "kv_compact",
+    "KvCache", "KvCache8", "kv_reserve", "kv_append", "kv_read", "kv_fork", "kv_free", "kv_compact",
     "attention_causal_varlen", "attention_decode_workspace", "attention_decode",
     "get_device_error", "new_error_word",
 ]
@@ -430,9 +430,21 @@ class KvCache:
         c._own()
         return c
 
+    # the C calls of this kind of cache
+    _calls = {name: f"rpp_kv_{name}" for name in ("reserve", "append", "read", "fork", "free", "compact",
+                                                  "compact_workspace_bytes")}
+    _calls |= {"decode": "rpp_attention_decode", "decode_workspace_bytes": "rpp_attention_decode_workspace_bytes"}
+
+    def _call(self, name):
+        return getattr(lib(), self._calls[name])
+
+    def _rows_dtype(self, dtype):
+        """The type of rows that go in and come out, given one, and how the C calls take it."""
+        return self._dtype, ()
+
     def _own(self):
         self.err = new_error_word(self.pool.device)
-        nbytes = lib().rpp_kv_compact_workspace_bytes(self._cfg)
+        nbytes = self._call("compact_workspace_bytes")(self._cfg)
         # kv_compact's lists: of the cache, as the calls that change one are ordered anyway
         self._remap = torch.empty(self.cfg.pages, dtype=torch.int32, device=self.pool.device)
         self._lists = torch.empty(nbytes, dtype=torch.uint8, device=self.pool.device)
@@ -449,17 +461,79 @@ class KvCache:
             raise ValueError("expected CUDA tensors on one device")
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         layers, pages, _, heads, rows, d = pool.shape
-        self.cfg = KvCfg(layers, pages, rows, heads, d, table.shape[0], table.shape[1], dtype_code(pool.dtype))
-        self._cfg = C.byref(self.cfg)
+        self.cfg = KvCfg(layers, pages, rows, heads, d, table.shape[0], table.shape[1], self._pool_code())
+        self._arrays = KvArrays(pool.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
+        self._dtype, self._d, self._width = pool.dtype, d, heads * d
+        self._bind_calls()
+
+    def _pool_code(self):
+        return dtype_code(self.pool.dtype)
+
+    def _bind_calls(self):
+        """What the C calls take."""
+        self._cfg, self._cache = C.byref(self.cfg), C.byref(self._arrays)
         if lib().rpp_kv_pool_bytes(self._cfg) == 0:
             raise RppError("rpp_kv_pool_bytes", _abi.RPP_EUNSUPPORTED)
-        self._arrays = KvArrays(pool.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
-        self._cache = C.byref(self._arrays)
-        self._dtype, self._d, self._width = pool.dtype, d, heads * d
 
     def adopt(self, table, refs):
         """Take the table and counts that kv_compact wrote to arrays of their own."""
         self._bind(self.pool, table, self.lens, refs)
+
+
+class KvCache8(KvCache):
+    """A paged key-value cache held in 8 bits (include/rpp.h, "The same cache held in 8 bits"): the pool of int8 or e4m3
+    codes and ``scales``, uint8 [layers, pages, 2, kv_heads, page_size // block], a scale byte for each ``block``
+    tokens of a head.  Every call of a KvCache takes it: rows and queries are fp16 or bf16."""
+
+    _calls = {name: call.replace("rpp_kv_", "rpp_kv8_").replace("decode", "decode8") for name, call in KvCache._calls.items()}
+    _codes = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+    def __init__(self, layers, pages, page_size, kv_heads, head_dim, slots, max_pages, dtype="e4m3", block=16,
+                 device="cuda"):
+        if dtype not in self._codes:
+            raise ValueError(f"dtype: expected one of {sorted(self._codes)}")
+        if block <= 0 or page_size % block:
+            raise ValueError("block: expected a divisor of page_size")
+        # (filled by the page: a byte of zeros is a scale, too)
+        self.scales = torch.zeros(layers, pages, 2, kv_heads, page_size // block, dtype=torch.uint8, device=device)
+        self._bind(torch.empty(layers, pages, 2, kv_heads, page_size, head_dim, dtype=self._codes[dtype], device=device),
+                   torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(slots, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device))
+        self._own()
+
+    @classmethod
+    def from_tensors(cls, pool, scales, table, lens, refs):
+        """A cache over arrays that the caller holds already (kept, not copied)."""
+        c = cls.__new__(cls)
+        c.scales = scales
+        c._bind(pool, table, lens, refs)
+        c._own()
+        return c
+
+    def _pool_code(self):
+        if self.pool.dtype not in self._codes.values():
+            raise ValueError("pool: expected int8 or float8_e4m3fn codes")
+        return RPP_I8 if self.pool.dtype is torch.int8 else RPP_E4M3
+
+    def _bind_calls(self):
+        scales, pool = self.scales, self.pool
+        if (scales.dim() != 5 or scales.shape[:4] != pool.shape[:4] or scales.dtype is not torch.uint8 or
+                not scales.is_contiguous() or scales.device != pool.device or not scales.shape[4] or
+                pool.shape[4] % scales.shape[4]):
+            raise ValueError("scales: expected a contiguous uint8 [layers, pages, 2, kv_heads, page_size // block] tensor "
+                             "beside the pool")
+        self.block = pool.shape[4] // scales.shape[4]
+        self._cfg8 = Kv8Cfg(self.cfg, self.block)
+        self._arrays8 = Kv8Arrays(self._arrays, scales.data_ptr())
+        self._cfg, self._cache = C.byref(self._cfg8), C.byref(self._arrays8)
+        if lib().rpp_kv8_pool_bytes(self._cfg) == 0:
+            raise RppError("rpp_kv8_pool_bytes", _abi.RPP_EUNSUPPORTED)
+
+    def _rows_dtype(self, dtype):
+        if dtype is not torch.float16 and dtype is not torch.bfloat16:
+            raise ValueError(f"expected fp16 or bf16 rows, got {dtype}")
+        return dtype, (RPP_F16 if dtype is torch.float16 else RPP_BF16,)
 
 
 def kv_reserve(cache: KvCache, slots, counts, err=None, stream=None):
@@ -467,9 +541,9 @@ def kv_reserve(cache: KvCache, slots, counts, err=None, stream=None):
     err = cache.err if err is None else err
     here = _here(cache.pool, slots, counts, err)
     n = slots.numel()
-    _check("rpp_kv_reserve", lib().rpp_kv_reserve(cache._cfg, cache._cache, _ints("slots", slots),
-                                                  _ints("counts", counts, n), n, err.data_ptr(),
-                                                  here if stream is None else stream.cuda_stream))
+    _check(cache._calls["reserve"], cache._call("reserve")(cache._cfg, cache._cache, _ints("slots", slots),
+                                                           _ints("counts", counts, n), n, err.data_ptr(),
+                                                           here if stream is None else stream.cuda_stream))
 
 
 def kv_append(cache: KvCache, layer: int, k, v, slots, cu_seqlens=None, err=None, stream=None):
@@ -481,13 +555,57 @@ def kv_append(cache: KvCache, layer: int, k, v, slots, cu_seqlens=None, err=None
     err = cache.err if err is None else err
     here = _here(cache.pool, k, v, slots, cu_seqlens, err)
     n, rows = slots.numel(), k.shape[0]
-    ld = _rows("k", k, cache._width, cache._dtype)
-    if _rows("v", v, cache._width, cache._dtype) != ld or v.shape[0] != rows:
+    dtype, code = cache._rows_dtype(k.dtype)
+    ld = _rows("k", k, cache._width, dtype)
+    if _rows("v", v, cache._width, dtype) != ld or v.shape[0] != rows:
         raise ValueError("k and v: expected equal row counts and strides")
-    _check("rpp_kv_append",
-           lib().rpp_kv_append(cache._cfg, cache._cache, layer, k.data_ptr(), v.data_ptr(), ld, _ints("slots", slots),
+    _check(cache._calls["append"],
+           cache._call("append")(cache._cfg, cache._cache, layer, k.data_ptr(), v.data_ptr(), *code, ld,
+                                 _ints("slots", slots),
+                                 None if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, n + 1), n, rows,
+                                 err.data_ptr(), here if stream is None else stream.cuda_stream))
+
+
+def kv_read(cache: KvCache, layer: int, slots, cu_seqlens=None, starts=None, rows=None, dtype=None, k=None, v=None,
+            err=None, stream=None):
+    """Rows of sequences read back from one layer, as kv_append takes them; returns (k, v).
+
+    Rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 (row i without cu_seqlens) receive the tokens of slots[i] from position
+    starts[i] on, or its last ones without starts.  k, v: where they go, [rows, kv_heads * head_dim]
+    each (columns of one wider tensor will do; rows behind the last sequence stay as they are); without
+    them a new tensor of ``rows`` rows (needed with cu_seqlens) and ``dtype`` (of a KvCache8: fp16 or bf16, bf16
+    by default) is made."""
+    err = cache.err if err is None else err
+    n, w = slots.numel(), cache._width
+    if (k is None) != (v is None):
+        raise ValueError("k and v: expected both or neither")
+    if k is None:
+        if rows is None:
+            if cu_seqlens is not None:
+                raise ValueError("rows: needed with cu_seqlens where k and v are not given")
+            rows = n
+        if dtype is None:
+            dtype = torch.bfloat16 if isinstance(cache, KvCache8) else cache._dtype
+        elif isinstance(dtype, str):
+            dtype = torch_dtype(dtype)
+        dtype, code = cache._rows_dtype(dtype)
+        both = _made(stream, torch.empty, (rows, 2 * w), dtype=dtype, device=cache.pool.device)
+        k, v = both[:, :w], both[:, w:]
+        ld = 2 * w
+    else:
+        rows = k.shape[0]
+        dtype, code = cache._rows_dtype(k.dtype)
+        ld = _rows("k", k, w, dtype)
+        if _rows("v", v, w, dtype) != ld or v.shape[0] != rows:
+            raise ValueError("k and v: expected equal row counts and strides")
+    here = _here(cache.pool, k, v, slots, cu_seqlens, starts, err)
+    _check(cache._calls["read"],
+           cache._call("read")(cache._cfg, cache._cache, layer, _ints("slots", slots),
+                               None if starts is None else _ints("starts", starts, n),
                                None if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, n + 1), n, rows,
-                               err.data_ptr(), here if stream is None else stream.cuda_stream))
+                               k.data_ptr(), v.data_ptr(), *code, ld, err.data_ptr(),
+                               here if stream is None else stream.cuda_stream))
+    return k, v
 
 
 def kv_fork(cache: KvCache, src, dst, err=None, stream=None):
@@ -495,16 +613,16 @@ def kv_fork(cache: KvCache, src, dst, err=None, stream=None):
     err = cache.err if err is None else err
     here = _here(cache.pool, src, dst, err)
     n = src.numel()
-    _check("rpp_kv_fork", lib().rpp_kv_fork(cache._cfg, cache._cache, _ints("src", src), _ints("dst", dst, n), n,
-                                            err.data_ptr(), here if stream is None else stream.cuda_stream))
+    _check(cache._calls["fork"], cache._call("fork")(cache._cfg, cache._cache, _ints("src", src), _ints("dst", dst, n), n,
+                                                     err.data_ptr(), here if stream is None else stream.cuda_stream))
 
 
 def kv_free(cache: KvCache, slots, err=None, stream=None):
     """Empty the slots; pages that no sequence uses any more become free."""
     err = cache.err if err is None else err
     here = _here(cache.pool, slots, err)
-    _check("rpp_kv_free", lib().rpp_kv_free(cache._cfg, cache._cache, _ints("slots", slots), slots.numel(),
-                                            err.data_ptr(), here if stream is None else stream.cuda_stream))
+    _check(cache._calls["free"], cache._call("free")(cache._cfg, cache._cache, _ints("slots", slots), slots.numel(),
+                                                     err.data_ptr(), here if stream is None else stream.cuda_stream))
 
 
 def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, live=None, err=None, stream=None):
@@ -521,11 +639,11 @@ def kv_compact(cache: KvCache, table_out=None, refs_out=None, remap=None, live=N
         live = _made(stream, torch.empty, 1, dtype=torch.int32, device=cache.pool.device)
     here = _here(cache.pool, table, refs, remap, live, err)
     cfg, lists = cache.cfg, cache._lists
-    _check("rpp_kv_compact",
-           lib().rpp_kv_compact(cache._cfg, cache._cache, _ints("table_out", table, cfg.slots * cfg.max_pages),
-                                _ints("refs_out", refs, cfg.pages), _ints("remap", remap, cfg.pages),
-                                _ints("live", live, 1), lists.data_ptr(), lists.numel(), err.data_ptr(),
-                                here if stream is None else stream.cuda_stream))
+    _check(cache._calls["compact"],
+           cache._call("compact")(cache._cfg, cache._cache, _ints("table_out", table, cfg.slots * cfg.max_pages),
+                                  _ints("refs_out", refs, cfg.pages), _ints("remap", remap, cfg.pages),
+                                  _ints("live", live, 1), lists.data_ptr(), lists.numel(), err.data_ptr(),
+                                  here if stream is None else stream.cuda_stream))
     return table, refs, live
 
 
@@ -557,15 +675,15 @@ def attention_causal_varlen(q, k, v, cu_seqlens, B: int, max_len: int, nh: int, 
 
 
 def attention_decode_workspace(cache: KvCache, n: int, nh: int) -> torch.Tensor:
-    nbytes = lib().rpp_attention_decode_workspace_bytes(cache._cfg, n, nh)
+    nbytes = cache._call("decode_workspace_bytes")(cache._cfg, n, nh)
     if nbytes == 0:
-        raise RppError("rpp_attention_decode_workspace_bytes", _abi.RPP_EINVAL)
+        raise RppError(cache._calls["decode_workspace_bytes"], _abi.RPP_EINVAL)
     return torch.empty(nbytes, dtype=torch.uint8, device=cache.pool.device)
 
 
 def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=None, workspace=None, err=None,
                      stream=None):
-    """Attention of one new token per sequence over the cache.
+    """Attention of one new token per sequence over the cache (a KvCache or a KvCache8).
 
     q: [n, nh * head_dim] (a column range of a QKV projection's output will do); slots:
     device int32[n], or None for slots 0 .. n - 1; scale: 1 / sqrt(head_dim) by default."""
@@ -577,11 +695,12 @@ def attention_decode(cache: KvCache, layer: int, q, slots=None, scale=None, out=
     if not ws.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     here = _here(cache.pool, q, slots, out, ws, err)
-    ld = _rows("q", q, nh * d, cache._dtype)
+    dtype, code = cache._rows_dtype(q.dtype)
+    ld = _rows("q", q, nh * d, dtype)
     o = _out_like(q, out, n, nh * d, stream)
-    _check("rpp_attention_decode",
-           lib().rpp_attention_decode(cache._cfg, cache._cache, layer, q.data_ptr(), ld,
-                                      None if slots is None else _ints("slots", slots, n), n, nh,
-                                      d ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), ws.nbytes,
-                                      err.data_ptr(), here if stream is None else stream.cuda_stream))
+    _check(cache._calls["decode"],
+           cache._call("decode")(cache._cfg, cache._cache, layer, q.data_ptr(), *code, ld,
+                                 None if slots is None else _ints("slots", slots, n), n, nh,
+                                 d ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                 err.data_ptr(), here if stream is None else stream.cuda_stream))
     return o

@@ -11,7 +11,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "librpp.so")
 
 RPP_OK, RPP_EINVAL, RPP_EUNSUPPORTED, RPP_ECUDA, RPP_EWORKSPACE, RPP_EDEVICE = 0, -1, -2, -3, -4, -5
-RPP_F32, RPP_F16, RPP_BF16, RPP_I8 = 0, 1, 2, 3
+RPP_F32, RPP_F16, RPP_BF16, RPP_I8, RPP_E4M3 = 0, 1, 2, 3, 4
 RPP_EPI_BIAS, RPP_EPI_BIAS_GELU, RPP_EPI_BIAS_RESIDUAL = 0, 1, 2
 RPP_DERR_LENGTH, RPP_DERR_TIMEOUT, RPP_DERR_ROWS, RPP_DERR_TMEM = 1, 2, 3, 4
 RPP_DERR_SLOT, RPP_DERR_PAGE, RPP_DERR_FULL = 5, 6, 7
@@ -48,6 +48,14 @@ class KvCfg(C.Structure):
 
 class KvArrays(C.Structure):
     _fields_ = [(n, vp) for n in ("pool", "table", "lens", "refs")]
+
+
+class Kv8Cfg(C.Structure):
+    _fields_ = [("kv", KvCfg), ("block", i32)]
+
+
+class Kv8Arrays(C.Structure):
+    _fields_ = [("kv", KvArrays), ("scales", vp)]
 
 
 class SwinSrc(C.Structure):
@@ -103,6 +111,21 @@ SIGNATURES = {
     "rpp_kv_free": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, i32, vp, vp]),
     "rpp_kv_compact_workspace_bytes": (sz, [C.POINTER(KvCfg)]),
     "rpp_kv_compact": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), vp, vp, vp, vp, vp, sz, vp, vp]),
+    "rpp_kv_read": (i32, [C.POINTER(KvCfg), C.POINTER(KvArrays), i32, vp, vp, vp, i32, i32, vp, vp, i32, vp, vp]),
+    "rpp_kv8_pool_bytes": (sz, [C.POINTER(Kv8Cfg)]),
+    "rpp_kv8_scales_bytes": (sz, [C.POINTER(Kv8Cfg)]),
+    "rpp_kv8_reserve": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), vp, vp, i32, vp, vp]),
+    "rpp_kv8_fork": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), vp, vp, i32, vp, vp]),
+    "rpp_kv8_free": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), vp, i32, vp, vp]),
+    "rpp_kv8_compact_workspace_bytes": (sz, [C.POINTER(Kv8Cfg)]),
+    "rpp_kv8_compact": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), vp, vp, vp, vp, vp, sz, vp, vp]),
+    "rpp_kv8_append": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), i32, vp, vp, i32, i32, vp, vp, i32, i32, vp,
+                             vp]),
+    "rpp_kv8_read": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), i32, vp, vp, vp, i32, i32, vp, vp, i32, i32, vp,
+                           vp]),
+    "rpp_attention_decode8_workspace_bytes": (sz, [C.POINTER(Kv8Cfg), i32, i32]),
+    "rpp_attention_decode8": (i32, [C.POINTER(Kv8Cfg), C.POINTER(Kv8Arrays), i32, vp, i32, i32, vp, i32, i32, f32, vp,
+                                    vp, sz, vp, vp]),
     "rpp_attention_causal_varlen": (i32, [vp, vp, vp, i32, i32, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp,
                                           vp]),
     "rpp_attention_decode_workspace_bytes": (sz, [C.POINTER(KvCfg), i32, i32]),

@@ -193,26 +193,48 @@ struct KvState {
   int32_t* lens;     // [slots]
   int32_t* refs;     // [pages]
 };
+// scales of a cache of 8-bit codes (kv8.cu); KvDims of such a cache: head_dim codes a row
+struct Kv8Scales {
+  uint8_t* scales;   // [layers, pages, 2, kv_heads, page_size >> shift]
+  int shift;         // log2 of the tokens that share one
+  bool i8;           // int8 codes, else e4m3
+};
 constexpr int kKvMaxList = 4096;      // entries of a slot list (held in shared memory)
 constexpr int kKvMaxSlots = 65536;    // slots of a cache (a bitmap of them is held in shared memory)
 cudaError_t launch_kv_reserve(const KvDims& d, const KvState& c, const int32_t* slots, const int32_t* counts, int n,
                               int32_t* err, cudaStream_t stream);
-cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* from, const int32_t* to, int n,
-                           int32_t* err, cudaStream_t stream);
+// q (fork, compact, read): null for a cache of 16-bit values
+cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const Kv8Scales* q, const int32_t* from, const int32_t* to,
+                           int n, int32_t* err, cudaStream_t stream);
 cudaError_t launch_kv_free(const KvDims& d, const KvState& c, const int32_t* slots, int n, int32_t* err,
                            cudaStream_t stream);
 cudaError_t launch_kv_append(const KvDims& d, const KvState& c, int layer, const void* k, const void* v,
                              int row_stride, const int32_t* slots, const int32_t* cu, int n, int rows_max,
                              int32_t* err, cudaStream_t stream);
 // moves: int32[2 + 2 * (pages / 2)] scratch, 8-byte aligned
-cudaError_t launch_kv_compact(const KvDims& d, const KvState& c, int32_t* table_out, int32_t* refs_out, int32_t* remap,
-                              int32_t* live, int32_t* moves, int32_t* err, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvDims& d, const KvState& c, const Kv8Scales* q, int32_t* table_out,
+                              int32_t* refs_out, int32_t* remap, int32_t* live, int32_t* moves, int32_t* err,
+                              cudaStream_t stream);
+
+cudaError_t launch_kv8_append(const KvDims& d, const KvState& s, const Kv8Scales& q, int layer, const void* k,
+                              const void* v, rpp_dtype dtype, int row_stride, const int32_t* slots, const int32_t* cu, int n,
+                              int rows_max, int32_t* err, cudaStream_t stream);
+// dtype: of k and v (without q the cache's)
+cudaError_t launch_kv_read(const KvDims& d, const KvState& s, const Kv8Scales* q, int layer, const int32_t* slots,
+                           const int32_t* starts, const int32_t* cu, int n, int rows_max, void* k, void* v,
+                           rpp_dtype dtype, int row_stride, int32_t* err, cudaStream_t stream);
 
 // single-token attention over a paged cache (attention_decode.cu); ws: attention_decode_ws_bytes
 size_t attention_decode_ws_bytes(int n, int nh, int nkv, int d);
 cudaError_t launch_attention_decode(const KvDims& d, const KvState& c, rpp_dtype dtype, int layer, const void* q,
                                     int q_stride, const int32_t* slots, int n, int nh, float scale, void* out,
                                     void* ws, int32_t* err, cudaStream_t stream);
+
+// the same over a cache of 8-bit codes (attention_decode8.cuh); dtype: of q and out
+size_t attention_decode8_ws_bytes(int n, int nh, int nkv, int d);
+cudaError_t launch_attention_decode8(const KvDims& d, const KvState& c, const Kv8Scales& q8, int layer, const void* q,
+                                     rpp_dtype dtype, int q_stride, const int32_t* slots, int n, int nh, float scale,
+                                     void* out, void* ws, int32_t* err, cudaStream_t stream);
 
 // causal attention over packed prompts (attention_causal.cu); strides in elements
 struct CausalArgs {

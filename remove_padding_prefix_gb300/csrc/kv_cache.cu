@@ -19,7 +19,10 @@
 // The lists a caller gives (slots, counts, cu_seqlens) and the state are read on the
 // device; every page number and position is checked against the pool before it is used,
 // so a list or a state that is wrong records a device error and never leaves the buffers.
-#include "kernels.h"
+//
+// A cache of 8-bit codes has the same state: its rows of head_dim codes move as rows of head_dim / 2 16-bit values, and
+// the calls that move rows move their blocks' scale bytes with them (PageScales).
+#include "kv_common.cuh"
 
 namespace rpp {
 
@@ -27,12 +30,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kMoveThreads = 256;
 
-__device__ __forceinline__ int used_pages(int len, int page_size) { return (len + page_size - 1) / page_size; }
-__device__ __forceinline__ bool len_ok(int len, const KvDims& d) {
-  return len >= 0 && static_cast<long long>(len) <= static_cast<long long>(d.max_pages) * d.page_size;
-}
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -46,43 +44,6 @@ __device__ __forceinline__ int warp_scan_incl(int v) {
     if (lane >= o) v += u;
   }
   return v;
-}
-
-// The first words of a kernel that takes a list of slots: one reading of the error word for the
-// whole CTA (other CTAs may set it at any time) and the list against the cache.  False if the CTA must
-// quit: the word is set, or a slot lies outside [0, d.slots) or is given twice, or cu[i + 1] < cu[i]
-// (recorded by one thread; every CTA of a launch comes to the same answer).  `seen`: (d.slots + 31) / 32
-// words of shared memory, left holding the slots given; cu: [n + 1] or null; first, c0, c1: slots[threadIdx.x]
-// and cu[threadIdx.x], cu[threadIdx.x + 1], read ahead by the caller so that the readings travel together.
-// Holds __syncthreads: called by all threads.
-struct Gate {
-  int quit, bad, back;
-};
-__device__ __forceinline__ bool pass(const int32_t* __restrict__ slots, int n, int first, const KvDims& d,
-                                     uint32_t* seen, Gate* g, int32_t* err, const int32_t* __restrict__ cu = nullptr,
-                                     int c0 = 0, int c1 = 0) {
-  if (threadIdx.x == 0) {
-    g->quit = device_error_set(err) ? 1 : 0;
-    g->bad = g->back = 0;
-  }
-  for (int i = threadIdx.x; i < (d.slots + 31) / 32; i += blockDim.x) seen[i] = 0u;
-  __syncthreads();
-  if (g->quit) return false;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int s = i == static_cast<int>(threadIdx.x) ? first : slots[i];
-    if (s < 0 || s >= d.slots || ((atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u)) g->bad = 1;
-    if (cu && (i == static_cast<int>(threadIdx.x) ? c1 < c0 : cu[i + 1] < cu[i])) g->back = 1;
-  }
-  __syncthreads();
-  if ((g->bad || g->back) && threadIdx.x == 0) set_device_error(err, g->bad ? RPP_DERR_SLOT : RPP_DERR_LENGTH);
-  return !g->bad && !g->back;
-}
-
-// One reading of the error word for the whole CTA.
-__device__ __forceinline__ bool quit(const int32_t* err, int* s_flag) {
-  if (threadIdx.x == 0) *s_flag = device_error_set(err) ? 1 : 0;
-  __syncthreads();
-  return *s_flag != 0;
 }
 
 // the four reference counts from page p on; pages past `pages` read as -1 (neither free nor live)
@@ -243,14 +204,22 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
+// The scale bytes of a cache of 8-bit codes, [layers, pages, 2 * kv heads, page rows >> shift]; no array for one of 16-bit
+// values.
+struct PageScales {
+  uint8_t* scales;
+  int shift;
+};
+
 // The shared part of each fork (table entries, reference counts) and the rows of its own
 // last page, in all layers.  blockIdx.x: pairs, grid-strided; blockIdx.y: shares of a pair's rows.  A pair's copy is
 // r rows (those past the last whole page) of d * 2 bytes in each of layers * 2 * kv heads
 // places; only those rows are moved.  What there is to do stands in the plan's marks, each taken away by
 // who has done it, so a wrong page number in one source (recorded) leaves the other pairs alone,
 // and a call that the plan refused finds no marks, whatever its lists and the state hold.
+template <bool kScales>
 __global__ void __launch_bounds__(kMoveThreads)
-    kv_fork_copy_kernel(KvDims d, uint4* __restrict__ pool, int32_t* __restrict__ table,
+    kv_fork_copy_kernel(KvDims d, PageScales q, uint4* __restrict__ pool, int32_t* __restrict__ table,
                         const int32_t* __restrict__ lens, int32_t* __restrict__ refs, const int32_t* __restrict__ from,
                         const int32_t* __restrict__ to, int n, int32_t* err) {
   pdl_wait();
@@ -313,6 +282,16 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (at[u] >= 0) dst[at[u]] = x[u];
+    }
+    if constexpr (kScales) {   // of the blocks that these rows begin
+      const int head = d.page_size >> q.shift, begun = ((rows - 1) >> q.shift) + 1;
+      const long long page = 2LL * d.kv_heads * head, layer = page * d.pages;
+      const long long bytes = static_cast<long long>(groups) * begun;
+      for (long long v = static_cast<long long>(blockIdx.y) * kMoveThreads + threadIdx.x; v < bytes; v += step) {
+        const long long g = v / begun, l = g / (2 * d.kv_heads);
+        const long long at = l * layer + (g - l * 2 * d.kv_heads) * head + (v - g * begun);
+        q.scales[pb * page + at] = q.scales[pa * page + at];
+      }
     }
     if (threadIdx.x == 0) atomicSub(&refs[pb], kForkShare);
   }
@@ -528,8 +507,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Moves the pages, and writes the table and the reference counts by the new numbers
 // (table_out and refs_out may be the arrays read).  A unit of the copy is 16 KB of a page
 // in one layer (or what is left of it): four 16-byte vectors a thread in flight.
+template <bool kScales>
 __global__ void __launch_bounds__(kMoveThreads)
-    kv_compact_move_kernel(KvDims d, uint4* __restrict__ pool, const int32_t* table,
+    kv_compact_move_kernel(KvDims d, PageScales q, uint4* __restrict__ pool, const int32_t* table,
                            const int32_t* __restrict__ lens, const int32_t* refs, int32_t* table_out,
                            int32_t* refs_out, const int32_t* __restrict__ remap, const int32_t* __restrict__ moves,
                            int32_t* err) {
@@ -562,6 +542,19 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (o + u * kMoveThreads < page_vec) dst[o + u * kMoveThreads] = x[u];
+    if constexpr (kScales) {
+      if (sub == 0) {
+        const int bytes = 2 * d.kv_heads * (d.page_size >> q.shift);   // of a page in one layer
+        const uint8_t* a = q.scales + (static_cast<long long>(layer) * d.pages + pr.y) * bytes;
+        uint8_t* b = q.scales + (static_cast<long long>(layer) * d.pages + pr.x) * bytes;
+        if (bytes % 4 == 0) {
+          for (int e = threadIdx.x; e < bytes / 4; e += kMoveThreads)
+            reinterpret_cast<uint32_t*>(b)[e] = reinterpret_cast<const uint32_t*>(a)[e];
+        } else {
+          for (int e = threadIdx.x; e < bytes; e += kMoveThreads) b[e] = a[e];
+        }
+      }
+    }
   }
   const long long entries = static_cast<long long>(d.slots) * d.max_pages;
   for (long long e = tid; e < entries; e += threads) {
@@ -592,11 +585,6 @@ __global__ void __launch_bounds__(kMoveThreads)
   }
 }
 
-inline int blocks_for(long long work, int most) {
-  if (work < 1) work = 1;
-  return static_cast<int>(work < most ? work : most);
-}
-
 }  // namespace
 
 cudaError_t launch_kv_reserve(const KvDims& d, const KvState& c, const int32_t* slots, const int32_t* counts, int n,
@@ -606,8 +594,17 @@ cudaError_t launch_kv_reserve(const KvDims& d, const KvState& c, const int32_t* 
                     slots, counts, n, 0, err);
 }
 
-cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* from, const int32_t* to, int n,
-                           int32_t* err, cudaStream_t stream) {
+// the sizes that the copies of 16-bit rows see
+inline KvDims as_16_bit(const KvDims& d, const Kv8Scales* q) {
+  KvDims r = d;
+  if (q) r.head_dim = d.head_dim / 2;
+  return r;
+}
+inline PageScales page_scales(const Kv8Scales* q) { return q ? PageScales{q->scales, q->shift} : PageScales{nullptr, 0}; }
+
+cudaError_t launch_kv_fork(const KvDims& dims, const KvState& c, const Kv8Scales* q, const int32_t* from,
+                           const int32_t* to, int n, int32_t* err, cudaStream_t stream) {
+  const KvDims d = as_16_bit(dims, q);
   // More CTAs than fit at once: the pairs' last pages are full to different degrees, and a share of
   // an empty one costs a CTA's start only.  16 prompts forked 8 times over 12 layers, with the free
   // before it: 73 us at 8 CTAs an SM, 66.6 at 16, 66.4 at 32, 75 at 64, 93 at 128; 4 forked twice 13.6 at each.
@@ -619,8 +616,8 @@ cudaError_t launch_kv_fork(const KvDims& d, const KvState& c, const int32_t* fro
   const cudaError_t e = launch_pdl(kv_reserve_kernel<true>, dim3(1), dim3(kPlanThreads), smem, stream, d, c.table,
                                    c.lens, c.refs, to, from, n, y, err);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_fork_copy_kernel, dim3(x, y), dim3(kMoveThreads), 0, stream, d, static_cast<uint4*>(c.pool),
-                    c.table, static_cast<const int32_t*>(c.lens), c.refs, from, to, n, err);
+  return launch_pdl(q ? kv_fork_copy_kernel<true> : kv_fork_copy_kernel<false>, dim3(x, y), dim3(kMoveThreads), 0, stream,
+                    d, page_scales(q), static_cast<uint4*>(c.pool), c.table, static_cast<const int32_t*>(c.lens), c.refs, from, to, n, err);
 }
 
 cudaError_t launch_kv_free(const KvDims& d, const KvState& c, const int32_t* slots, int n, int32_t* err,
@@ -646,13 +643,15 @@ cudaError_t launch_kv_append(const KvDims& d, const KvState& c, int layer, const
                     tok, err);
 }
 
-cudaError_t launch_kv_compact(const KvDims& d, const KvState& c, int32_t* table_out, int32_t* refs_out, int32_t* remap,
-                              int32_t* live, int32_t* moves, int32_t* err, cudaStream_t stream) {
+cudaError_t launch_kv_compact(const KvDims& dims, const KvState& c, const Kv8Scales* q, int32_t* table_out,
+                              int32_t* refs_out, int32_t* remap, int32_t* live, int32_t* moves, int32_t* err,
+                              cudaStream_t stream) {
+  const KvDims d = as_16_bit(dims, q);
   cudaError_t e = launch_pdl(kv_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, d.pages,
                              static_cast<const int32_t*>(c.refs), remap, live, moves, static_cast<const int32_t*>(err));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_compact_move_kernel, dim3(8 * num_sms()), dim3(kMoveThreads), 0, stream, d,
-                    static_cast<uint4*>(c.pool), static_cast<const int32_t*>(c.table),
+  return launch_pdl(q ? kv_compact_move_kernel<true> : kv_compact_move_kernel<false>, dim3(8 * num_sms()),
+                    dim3(kMoveThreads), 0, stream, d, page_scales(q), static_cast<uint4*>(c.pool), static_cast<const int32_t*>(c.table),
                     static_cast<const int32_t*>(c.lens), static_cast<const int32_t*>(c.refs), table_out, refs_out,
                     static_cast<const int32_t*>(remap), static_cast<const int32_t*>(moves), err);
 }
