@@ -38,9 +38,10 @@ namespace rpp {
 
 namespace {
 
+constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;       // K then V, 4 KB each
-constexpr size_t kRingBytes = static_cast<size_t>(kLineWarps) * kStages * kStageBytes;
+constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kStageBytes;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -86,7 +87,7 @@ __device__ __forceinline__ void split2(float lo, float hi, uint32_t* p, uint32_t
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kLineWarps * 32, 1) attention_decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const DecodeParams p) {
   constexpr int KB = kStageBytes / (4 * D);      // keys of a block: 16 or 32
   constexpr int NT = KB / 8;                     // 8-key tiles of a block
   constexpr int CH = D / 8;                      // 16-byte chunks of a row
@@ -99,12 +100,12 @@ __global__ void __launch_bounds__(kLineWarps * 32, 1) attention_decode_kernel(co
   const int warp = warp_id(), lane = lane_id();
   pdl_wait();
   pdl_trigger();
-  const long long carry = line_plan<T, D, KB>(p, s_pre);
+  const long long carry = line_plan<T, D, KB, kWarps>(p, s_pre);
   if (carry < 0) return;
   const int per_seq = p.d.kv_heads * p.parts;    // units (kv head, 16-head part) of a sequence
   const long long total = carry * per_seq;
   if (total == 0) return;
-  const long long warps = share_warps(total, static_cast<long long>(gridDim.x) * kLineWarps);
+  const long long warps = share_warps(total, static_cast<long long>(gridDim.x) * kWarps);
   // consecutive shares go to different SMs: warp w of CTA c has share w * CTAs + c
   const long long w_id = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
   if (w_id >= warps) return;
@@ -435,15 +436,15 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
       limit.raise(attention_decode_kernel<T, D>, kRingBytes + (kKvMaxList + 1) * sizeof(long long));
   if (a != cudaSuccess) return a;
   const int ctas = decode_ctas();
-  const cudaError_t e = launch_pdl(attention_decode_kernel<T, D>, dim3(ctas), dim3(kLineWarps * 32), smem, stream, p);
+  const cudaError_t e = launch_pdl(attention_decode_kernel<T, D>, dim3(ctas), dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_join<T, D>(p, ctas * kLineWarps, stream);
+  return launch_join<T, D>(p, ctas * kWarps, stream);
 }
 
 }  // namespace
 
 size_t attention_decode_ws_bytes(int n, int nh, int nkv, int d) {
-  return line_ws_bytes(n, nh, nkv, d, static_cast<long long>(decode_ctas()) * kLineWarps);
+  return line_ws_bytes(n, nh, nkv, d, static_cast<long long>(decode_ctas()) * kWarps);
 }
 
 cudaError_t launch_attention_decode(const KvDims& d, const KvState& c, rpp_dtype dtype, int layer, const void* q,
@@ -464,7 +465,7 @@ cudaError_t launch_attention_decode(const KvDims& d, const KvState& c, rpp_dtype
   p.parts = (p.group + kRows - 1) / kRows;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
-  line_ws_bind(&p, ws, static_cast<long long>(decode_ctas()) * kLineWarps);
+  line_ws_bind(&p, ws, static_cast<long long>(decode_ctas()) * kWarps);
   p.err = err;
   if (dtype == RPP_F16)
     return d.head_dim == 64 ? launch<__half, 64>(p, stream) : launch<__half, 128>(p, stream);

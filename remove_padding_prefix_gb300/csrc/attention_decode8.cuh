@@ -7,20 +7,25 @@
 //
 //  * Work is cut as there (decode_line.cuh), in blocks of 2 KB of K and 2 KB of V.
 //  * Products are transposed: S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16, keys (or head columns) as the 16 rows and
-//    up to 8 query heads as the 8 columns, two such for 9 to 16.  The cache is then the operand whose rows a lane holds
-//    whole: the order of a contraction and the order of the result's rows are free, so a lane reads 16
-//    contiguous bytes of a row from global memory and those are its operand as they are, without shared memory:
-//    for K the columns 16 t .. of key rows g and g + 8 (Q's fragments take the same order), for V the columns
-//    16 g .. of four keys, paired across keys by byte permutations (the output's rows take that order).
+//    up to 8 query heads as the 8 columns, two such for 9 to 16.  The order of a contraction and the order of the
+//    result's rows are free, so a lane's operands are 16 bytes of a row as they lie there: of K the columns 16 t .. of
+//    key rows g and g + 8 (Q's fragments take the same order), of V the columns 16 g .. of four keys, paired across
+//    keys by byte permutations (the output's rows take that order).
+//  * A warp keeps its own ring of blocks (cp.async, 16 bytes a lane), chunks moved inside their 128-byte line so that no
+//    reading meets a bank twice: 192 KB an SM on their way or in use.  Reading the cache straight into operand
+//    registers, without the ring, leaves too few bytes on their way: 128 sequences of 200 to 8192 keys, d = 128, 32 heads
+//    on 8, e4m3: 238 us against 190; with blocks brought to L2 ahead of that by bulk prefetches: 275 and more.
 //  * Codes become f16 (exact for both types), so the products are exact in fp32.  fp16 queries are taken as they are; a bf16
-//    query head is multiplied by the power of two that brings its largest element to 2^14 .. 2^15 (what that leaves below
-//    f16's smallest step is under 2^-38 of the largest) and its scores by the inverse.
+//    query head is multiplied by the power of two that brings its largest element to 2^7 .. 2^8 (what that leaves below
+//    f16's smallest step is under 2^-31 of the largest) and its scores by the inverse.
 //  * K's scale multiplies the scores in fp32.  V's multiplies the weights, p 2^(vb - E) with E the largest vb so far,
 //    before they become f16 operands; E moves as the running maximum does, and 2^E multiplies the output at the end.
-//  * The maximum moves only when a score passes it by more than 8 (log2 units), asked by one vote a
-//    block; its reduction over the lanes runs only then.
+//  * The maximum moves only when a lane's weights of a block (2 or 4 of a head) add up to more than 2^8 times the largest
+//    one's at the last move; so asks one vote a block, with whether V's scale moves, and the reductions over
+//    the lanes run only then.
 //  * P^T comes out of the scores' registers by two 8 x 8 transposes (movmatrix).  P is split into two f16
-//    parts (p and what rounding p left), as in the 16-bit kernel.
+//    parts (p and what rounding p left), as in the 16-bit kernel; that costs nothing in the batch above, and 2 us of 61 for
+//    131000 keys of 16 heads, int8, d = 64.
 //
 // Codes past the sequence may be anything: their scores are -inf, their codes zeros.
 #pragma once
@@ -35,19 +40,27 @@ struct Decode8Params : DecodeParams {
   const uint8_t* scales;     // of the layer
   int shift;                 // log2 of a block's tokens
   int bf16;                  // type of q and out
+  long long page_bytes, head_bytes, v_bytes;      // in the pool: of a page, of a head in it, from K to V
+  int page_scales, head_scales, v_scales;         // and among the scales
 };
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+__device__ __forceinline__ uint4 ld_shared4(uint32_t a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_stream2(const uint8_t* p) {
+__device__ __forceinline__ uint2 ld_shared2(uint32_t a) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ uint32_t ld_shared1(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void mma8(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -55,6 +68,14 @@ __device__ __forceinline__ void mma8(float* c, uint32_t a0, uint32_t a1, uint32_
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same onto zero
+__device__ __forceinline__ void mma8_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -67,137 +88,177 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 }
 
 constexpr int kBlockBytes = 2048;                            // of K, and of V
-// CTAs an SM: two while a unit has up to 8 query heads (its registers fit twice)
-inline int decode8_ctas(int group) { return num_sms() * (group <= 8 ? 2 : 1); }
+// Warps of a CTA (one an SM) and stages of a warp's ring: 16 warps of 128 registers while a unit has up to 8 query heads,
+// 8 of 255 for more; 192 KB of codes on their way to an SM, or in use, either way.
+template <int NT> struct Shape8 {
+  static constexpr int kWarps = NT == 1 ? 16 : 8, kStages = NT == 1 ? 3 : 6;
+};
+constexpr size_t kScaleBytes = 256;                          // of a stage: K's and V's of up to 32 keys, 4 bytes each
+template <int NT> constexpr size_t ring8_bytes() {
+  return Shape8<NT>::kWarps * Shape8<NT>::kStages * (2 * kBlockBytes + kScaleBytes);
+}
+constexpr int kPrefixMax = 2048;                             // longer lists keep their prefix in the workspace
+inline int decode8_warps(int group) { return num_sms() * (group <= 8 ? Shape8<1>::kWarps : Shape8<2>::kWarps); }
 
-template <bool kI8, int D, int NT, bool kFine>
-__global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_decode8_kernel(const Decode8Params p) {
+template <bool kI8, int D, int NT>
+__global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_kernel(const Decode8Params p) {
+  constexpr int W = Shape8<NT>::kWarps, kStages = Shape8<NT>::kStages;
   constexpr int KB = kBlockBytes / D;            // keys of a block: 16 or 32
   constexpr int G = KB / 16;                     // groups of 16 keys
   constexpr int KS = D / 16;                     // k16 steps of the scores, and 16-row tiles of the output
   constexpr int CW = D / 32;                     // words of V that a lane has of a key
-  constexpr int SC = kFine ? 2 : 1;              // scales a lane needs of 16 keys
-  constexpr float kUp = 7.f;                     // weights (and their sum) are kept 2^7 times as large, up to 2^15
+  constexpr int CH = D / 16, RG = 32 / CH;       // 16-byte chunks of a row, rows that the lanes copy at once
+  constexpr float kUp = 7.f;                     // weights (and their sum) are kept 2^7 times as large;
+  constexpr float kMost = 32768.f;               // where a lane's of a block add up to more, the maximum moves
+  constexpr int kNaN = 255 << 23;
   const float kNone = __int_as_float(0xff800000);
-  extern __shared__ __align__(16) uint8_t smem[];
-  long long* s_pre = reinterpret_cast<long long*>(smem);    // [n + 1]
+  extern __shared__ __align__(1024) uint8_t smem[];
+  long long* s_pre = p.n <= kPrefixMax ? reinterpret_cast<long long*>(smem + ring8_bytes<NT>()) : p.prefix;   // [n + 1]
   const int warp = warp_id(), lane = lane_id();
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();
-  const long long carry = line_plan<__half, D, KB>(p, s_pre);   // (zeros are the same in both types)
+  const long long carry = line_plan<__half, D, KB, W>(p, s_pre);   // (zeros are the same in both types)
   if (carry < 0) return;
   const int per_seq = p.d.kv_heads * p.parts;
   const long long total = carry * per_seq;
   if (total == 0) return;
-  const long long warps = share_warps(total, static_cast<long long>(gridDim.x) * kLineWarps);
+  const long long warps = share_warps(total, static_cast<long long>(gridDim.x) * W);
   const long long w_id = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
   if (w_id >= warps) return;
   const long long f0 = share_start(total, warps, w_id), f1 = share_start(total, warps, w_id + 1);
 
-  LineCursor ld{};                  // the block to load next
-  ld.start(p, s_pre, per_seq, f0);
-  LineCursor cc = ld;               // the block being computed
-  if (lane == 0) p.cuts[w_id] = make_int4(ld.blk > 0 ? ld.i : -1, ld.unit, ld.blk, 0);
-
+  // ---- the block to load next
+  LineCursor first{};
+  first.start(p, s_pre, per_seq, f0);
+  if (lane == 0) p.cuts[w_id] = make_int4(first.blk > 0 ? first.i : -1, first.unit, first.blk, 0);
+  struct Place {
+    int i, unit, len, left;         // sequence, unit, its keys, keys from the block on
+  };
+  Place ld{first.i, first.unit, first.len, first.len - first.blk * KB};
+  Place cc = ld;                    // the block being computed
+  bool whole = first.blk == 0, later = false;   // its unit begins in this share; with a block behind the share's first
+  const int32_t* table = first.row;
   const int ps = p.d.page_size;
-  const uint8_t* pool = static_cast<const uint8_t*>(p.pool);
-  const long long head_bytes = static_cast<long long>(ps) * D;
-  const long long v_off = p.d.kv_heads * head_bytes;
-  const int head_scales = ps >> p.shift, v_scales = p.d.kv_heads * head_scales;
-  int page[G], row[G];              // of the block to load next
-  auto read_pages = [&](const LineCursor& c) {
+  const int lc = lane % CH, lr = lane / CH;      // chunk and row of a lane inside a row group
+  const uint8_t *kp, *sp;           // of the unit to load, in page 0: this lane's chunk of K's first rows; its scale
+  int at, row;                      // its next 16 keys: which of the sequence's pages, and the row in it
+  int page[G], rows[G];             // of the block to load next
+  auto enter_unit = [&]() {
+    const int head = ld.unit / p.parts;
+    kp = static_cast<const uint8_t*>(p.pool) + head * p.head_bytes + lr * D + lc * 16;
+    sp = p.scales + static_cast<long long>(head) * p.head_scales + (lane < 16 ? 0 : p.v_scales);
+    const int key = ld.len - ld.left;
+    at = key / ps;
+    row = key - at * ps;
+  };
+  // the next unit: the sequence's, or the first of the next sequence that is not empty
+  auto next_unit = [&](Place& c) {
+    if (++c.unit == per_seq) {
+      c.unit = 0;
+      do ++c.i;
+      while (c.i < p.n - 1 && s_pre[c.i + 1] == s_pre[c.i]);
+      int slot;
+      c.len = seq_len(p, c.i, &slot);
+    }
+    c.left = c.len;
+  };
+  auto advance = [&]() {            // to the next block of the line (only while there is one)
+    ld.left -= KB;
+    if (ld.left > 0) return;
+    const int i = ld.i;
+    next_unit(ld);
+    if (ld.i != i) table = p.table + static_cast<long long>(p.slots ? p.slots[ld.i] : ld.i) * p.d.max_pages;
+    enter_unit();
+  };
+  auto read_pages = [&]() {
 #pragma unroll
     for (int s = 0; s < G; ++s) {
-      const int key = c.blk * KB + 16 * s;
-      page[s] = 0;
-      row[s] = 0;
-      if (key < c.len) {
-        const int at = key / ps;
-        page[s] = __ldg(c.row + at);
-        row[s] = key - at * ps;
+      page[s] = 16 * s < ld.left ? __ldg(table + at) : 0;    // past the sequence's end any page will do
+      rows[s] = row;
+      row += 16;
+      if (row == ps) {
+        row = 0;
+        ++at;
       }
     }
   };
-  uint32_t kr[16], vr[16];          // the block's codes: this lane's part
-  int kb[G][SC], vb[G][SC];         // and scale bytes (keys g, g + 8 of 16)
-  auto head_of = [&](const LineCursor& c, int s) {
-    if (page[s] < 0 || page[s] >= p.d.pages) {
-      if (lane == 0) set_device_error(p.err, RPP_DERR_PAGE);
-      page[s] = 0;
-    }
-    return static_cast<long long>(page[s]) * 2 * p.d.kv_heads + c.unit / p.parts;
-  };
-  auto load_k = [&](const LineCursor& c) {
+  // ---- loads: a warp's ring of kStages blocks, K then V, in 128-byte lines of eight 16-byte chunks.  Chunks are moved inside
+  // their line so that the eight lanes that read at once meet all eight: D = 128, K by the row's parity (lanes g, g + 1
+  // want the same four chunks), V by twice the row pair (lanes t want the same two); D = 64, a line is two rows, by
+  // twice the line.
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * kBlockBytes);
+  const uint32_t ring_sc = smem_u32(smem) + W * kStages * 2 * kBlockBytes + warp * (kStages * kScaleBytes);
+  const uint32_t k_to = D == 128 ? lr * 128 + ((lc ^ ((lr & 1) << 2)) << 4)
+                                 : (lr >> 1) * 128 + ((((lr & 1) * 4 + lc) ^ (lr & 6)) << 4);
+  const uint32_t v_to = kBlockBytes + (D == 128 ? lr * 128 + ((lc ^ (lr & 2)) << 4) : k_to);
+  int sc[G], sc_left;               // the scale bytes on their way: of lane & 15's key, K's below lane 16, V's from there
+  uint32_t sc_to = 0;
+  auto issue = [&](int stage) {
+    const uint32_t to = ring + stage * (2 * kBlockBytes);
 #pragma unroll
     for (int s = 0; s < G; ++s) {
-      const long long head = head_of(c, s);
-      const uint8_t* src = pool + head * head_bytes + (row[s] + g) * D + t * 16;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const uint4 v = ld_stream(src + 8 * h * D + 64 * x);
-          uint32_t* to = kr + ((s * 2 + h) * (D / 64) + x) * 4;
-          to[0] = v.x;
-          to[1] = v.y;
-          to[2] = v.z;
-          to[3] = v.w;
-        }
-      const uint8_t* sc = p.scales + head * head_scales;
-#pragma unroll
-      for (int h = 0; h < SC; ++h) kb[s][h] = __ldg(sc + ((row[s] + (kFine ? g + 8 * h : 0)) >> p.shift));
-    }
-  };
-  auto load_v = [&](const LineCursor& c) {
-#pragma unroll
-    for (int s = 0; s < G; ++s) {
-      const long long head = head_of(c, s);
-      const uint8_t* src = pool + head * head_bytes + v_off + (row[s] + 2 * t) * D + g * (D / 8);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {              // keys 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint8_t* a = src + ((j & 1) + 8 * (j >> 1)) * D;
-        uint32_t* to = vr + (s * 4 + j) * CW;
-        if constexpr (CW == 4) {
-          const uint4 v = ld_stream(a);
-          to[0] = v.x;
-          to[1] = v.y;
-          to[2] = v.z;
-          to[3] = v.w;
-        } else {
-          const uint2 v = ld_stream2(a);
-          to[0] = v.x;
-          to[1] = v.y;
-        }
+      if (static_cast<unsigned>(page[s]) >= static_cast<unsigned>(p.d.pages)) {
+        if (lane == 0) set_device_error(p.err, RPP_DERR_PAGE);
+        page[s] = 0;
       }
-      const uint8_t* sc = p.scales + head * head_scales + v_scales;
+      const uint8_t* k = kp + page[s] * p.page_bytes + rows[s] * D;
+      const uint8_t* v = k + p.v_bytes;
 #pragma unroll
-      for (int h = 0; h < SC; ++h) vb[s][h] = __ldg(sc + ((row[s] + (kFine ? g + 8 * h : 0)) >> p.shift));
+      for (int i = 0; i < 16 / RG; ++i) {
+        copy16(to + k_to + s * 1024 + i * 512, k + i * RG * D);
+        copy16(to + (D == 128 && (i & 1) ? v_to ^ 64 : v_to) + s * 1024 + i * 512, v + i * RG * D);
+      }
+      sc[s] = __ldg(sp + static_cast<long long>(page[s]) * p.page_scales + ((rows[s] + (lane & 15)) >> p.shift));
+    }
+    sc_left = ld.left;
+    sc_to = ring_sc + stage * kScaleBytes + lane * 4;
+  };
+  // K's as the float 2^(b - 126), V's shifted as far; 255 in either makes V's 255.  Keys past the sequence: of no effect (K's
+  // is large, so that its product with any qs is above 0 and that with a score of -inf is -inf).
+  auto keep_scales = [&]() {
+#pragma unroll
+    for (int s = 0; s < G; ++s) {
+      const int other = __shfl_xor_sync(0xffffffffu, sc[s], 16);
+      int x = lane < 16 ? sc[s] + 1 : other == 255 ? 255 : sc[s];
+      if (16 * s + (lane & 15) >= sc_left) x = lane < 16 ? 253 : 0;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc_to + s * 128), "r"(x << 23) : "memory");
     }
   };
 
-  long long lf = f0 + 1;            // next block to load
-  read_pages(ld);
-  load_k(ld);
-  load_v(ld);
-  if (lf < f1) {
-    ld.advance(p, s_pre, per_seq);
-    read_pages(ld);
+  long long todo = f1 - f0;         // blocks from the one being computed on
+  enter_unit();
+  read_pages();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < todo) {
+      if (s) keep_scales();
+      issue(s);
+      if (s + 1 < todo) {
+        advance();
+        read_pages();
+      }
+    }
+    cp_async_commit();
   }
+  int stage = 0;
+  // this lane's operands in a stage
+  const uint32_t k_at = D == 128 ? g * 128 + ((t + ((g & 1) << 2)) << 4) : (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (g & 6)) << 4);
+  const uint32_t v_at = kBlockBytes + (D == 128 ? 2 * t * 128 + ((g ^ (2 * t)) << 4) : t * 128 + (((g >> 1) ^ (2 * t)) << 4) + (g & 1) * 8);
 
   const int rows_kept = p.group < kRows ? p.group : kRows;
   uint32_t qf[NT][KS][2];
-  float qs[NT][2];                  // scale (to base 2) of the scores of query heads 2t, 2t + 1
+  float qs[NT][2];                  // scale (to base 2) of the scores of query heads 2t, 2t + 1, times 1/2
   float o[NT][KS][4];               // heads 2t, 2t + 1 of an even column, then of the odd one after it
-  float m[NT][2], l[NT][2];
-  int E = 0;                        // output and weights are in units of 2^(E - 127)
-  bool fresh = true, whole = false;
-  for (long long f = f0; f < f1; ++f) {
-    const int head = cc.unit / p.parts, part = cc.unit - head * p.parts;
-    const int have = min(kRows, p.group - part * kRows);
+  float l[NT][2];                   // sums of the weights 2^(score + n):
+  float n[NT][2];                   // kUp - maximum; +inf before the first one, so that any score passes kMost
+  int E = 0;                        // output and weights are in units of 2^(e - 127), E = e << 23
+  bool fresh = true;
+  for (; todo > 0; --todo) {
     if (fresh) {
+      const int head = cc.unit / p.parts, part = cc.unit - head * p.parts;
+      const int have = min(kRows, p.group - part * kRows);
       fresh = false;
-      whole = cc.blk == 0;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<long long>(cc.i) * p.q_stride +
                           static_cast<long long>(head * p.group + part * kRows) * D;
 #pragma unroll
@@ -215,7 +276,7 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
             w[x * 8 + y * 4 + 2] = v.z;
             w[x * 8 + y * 4 + 3] = v.w;
           }
-        float back = p.scale_log2;
+        float back = p.scale_log2 * 0.5f;
         if (p.bf16) {
           uint32_t most = 0;
 #pragma unroll
@@ -223,7 +284,7 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
           most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
           most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
           const int field = most >> 7;           // of the largest element; 255: no number, its head's output is NaN
-          const int up = field == 255 ? 0 : min(14 + 127 - field, 126);
+          const int up = field == 255 ? 0 : min(7 + 127 - field, 110);   // (at 110 every bf16 is exact)
           const float f_up = __int_as_float((127 + up) << 23);
           back *= __int_as_float((127 - up) << 23);
 #pragma unroll
@@ -237,8 +298,8 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          qs[nt][c] = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
-          m[nt][c] = kNone;
+          qs[nt][c] = fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + c) * 4), 1.4e-45f);
+          n[nt][c] = __int_as_float(0x7f800000);
           l[nt][c] = 0.f;
         }
 #pragma unroll
@@ -248,76 +309,98 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
       }
       E = 0;
     }
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    keep_scales();                  // of the last block that was issued
+    __syncwarp();
+    {   // into the stage that the last block freed
+      if (todo >= kStages) {
+        issue(stage == 0 ? kStages - 1 : stage - 1);
+        if (todo > kStages) {
+          advance();
+          read_pages();
+        }
+      }
+      cp_async_commit();
+    }
+    const uint32_t here = ring + stage * (2 * kBlockBytes), here_sc = ring_sc + stage * kScaleBytes + g * 4;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     // ---- scores: KB keys x 8 NT heads
     float sc[G][NT][4];
+    float ks[G][2];                 // scales of keys g, g + 8: 2^(b - 126)
+    int vs[G][2];                   // of V: b << 23
 #pragma unroll
     for (int s = 0; s < G; ++s) {
+      uint32_t kr[2][KS];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[s][nt][e] = 0.f;
+        for (int x = 0; x < D / 64; ++x) {
+          const uint4 v = ld_shared4(here + (x ? k_at ^ 64 : k_at) + s * 1024 + h * 8 * D);
+          kr[h][4 * x] = v.x;
+          kr[h][4 * x + 1] = v.y;
+          kr[h][4 * x + 2] = v.z;
+          kr[h][4 * x + 3] = v.w;
+        }
+        ks[s][h] = __uint_as_float(ld_shared1(here_sc + s * 128 + h * 32));
+        vs[s][h] = ld_shared1(here_sc + s * 128 + 64 + h * 32);
+      }
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const uint2 a = decode4<kI8>(kr[(s * 2 * KS) + k]), b = decode4<kI8>(kr[(s * 2 + 1) * KS + k]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma8(sc[s][nt], a.x, b.x, a.y, b.y, qf[nt][k][0], qf[nt][k][1]);
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < G; ++s)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float ks = scale_of(kb[s][kFine ? h : 0]);
+        const uint2 a = decode4<kI8>(kr[0][k]), b = decode4<kI8>(kr[1][k]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) sc[s][nt][2 * h + c] *= ks * qs[nt][c];
-      }
-    int vs[G][2];                   // V's scale bytes of keys g, g + 8
-#pragma unroll
-    for (int s = 0; s < G; ++s)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) vs[s][h] = vb[s][kFine ? h : 0];
-    const int left = cc.len - cc.blk * KB;
-    if (left < KB) {                // keys past the sequence: no score, no scale, codes zero
-#pragma unroll
-      for (int s = 0; s < G; ++s) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (16 * s + g + 8 * h < left) continue;
-          vs[s][h] = 0;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sc[s][nt][2 * h] = sc[s][nt][2 * h + 1] = kNone;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (16 * s + 2 * t + (j & 1) + 8 * (j >> 1) >= left)
-#pragma unroll
-            for (int w = 0; w < CW; ++w) vr[(s * 4 + j) * CW + w] = 0u;
+          if (k == 0) mma8_first(sc[s][nt], a.x, b.x, a.y, b.y, qf[nt][k][0], qf[nt][k][1]);
+          else mma8(sc[s][nt], a.x, b.x, a.y, b.y, qf[nt][k][0], qf[nt][k][1]);
       }
     }
-    if (lf < f1) load_k(ld);
-    // ---- running maximum and V's scale, lazily moved
-    bool move = false;
-#pragma unroll
-    for (int s = 0; s < G; ++s)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        move = move || (vs[s][h] > E && vs[s][h] != 255);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) move = move || sc[s][nt][2 * h + c] > m[nt][c] + 8.f;
-      }
-    if (__any_sync(0xffffffffu, move)) {
-      int e1 = E;
+    const int left = cc.left;
+    if (left < KB) {                // keys past the sequence: no score
 #pragma unroll
       for (int s = 0; s < G; ++s)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (vs[s][h] != 255) e1 = max(e1, vs[s][h]);
+          if (16 * s + g + 8 * h >= left)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) sc[s][nt][2 * h] = sc[s][nt][2 * h + 1] = kNone;
+    }
+    // ---- weights
+    float w[G][NT][4], sum[NT][2];
+    bool slow = false;
+    auto weigh = [&](int nt, int c) {
+      sum[nt][c] = 0.f;
+#pragma unroll
+      for (int s = 0; s < G; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[s][nt][2 * h + c] = ex2_approx(fmaf(sc[s][nt][2 * h + c], ks[s][h] * qs[nt][c], n[nt][c]));
+          sum[nt][c] += w[s][nt][2 * h + c];
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < G; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) slow = slow || vs[s][h] > E;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        weigh(nt, c);
+        slow = slow || sum[nt][c] > kMost;
+      }
+    if (__any_sync(0xffffffffu, slow)) {
+      // the maximum or V's largest scale moves (or the unit has a block of NaN)
+      int e1 = E;
+      bool bad = false;
+#pragma unroll
+      for (int s = 0; s < G; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (vs[s][h] != kNaN) e1 = max(e1, vs[s][h]);
+          bad = bad || vs[s][h] == kNaN;
+        }
       e1 = __reduce_max_sync(0xffffffffu, e1);
-      const float ae = pow2_neg(e1 - E);
+      const float ae = pow2_neg((e1 - E) >> 23), spoil = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
       E = e1;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -326,16 +409,19 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
         for (int c = 0; c < 2; ++c) {
           float mx = kNone;
 #pragma unroll
-          for (int s = 0; s < G; ++s) mx = fmaxf(mx, fmaxf(sc[s][nt][c], sc[s][nt][2 + c]));
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, sc[s][nt][2 * h + c] * (ks[s][h] * qs[nt][c]));
 #pragma unroll
           for (int x = 4; x <= 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
           a[c] = 1.f;
-          if (mx > m[nt][c] + 8.f) {
-            a[c] = ex2_approx(m[nt][c] - mx);
-            m[nt][c] = mx;
+          if (mx + n[nt][c] > kUp + 6.f) {       // (not NaN: +inf on -inf)
+            a[c] = ex2_approx(kUp - mx - n[nt][c]);
+            n[nt][c] = kUp - mx;
           }
-          l[nt][c] *= a[c];
+          l[nt][c] = fmaf(l[nt][c], a[c], spoil);
           a[c] *= ae;
+          weigh(nt, c);
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k)
@@ -343,43 +429,59 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
           for (int e = 0; e < 4; ++e) o[nt][k][e] *= a[e & 1];
       }
     }
-    // ---- weights, and their transposes as operands
+    // ---- and their transposes as operands, in units of V's largest scale
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) l[nt][c] += sum[nt][c];
     uint32_t ph[G][NT][2], pl[G][NT][2];
 #pragma unroll
     for (int s = 0; s < G; ++s)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // at most 1, as E is at least each (NaN of 255)
-        const float f = vs[s][h] == 255 ? __int_as_float(0x7fffffff) : pow2_neg(E - vs[s][h]);
+        const float f = __int_as_float(max(vs[s][h] - E + (127 << 23), 0));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float w[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // a head whose scores so far are all -inf (or no numbers) keeps m = -inf: 0, not 2^(-inf + inf)
-            const float n = m[nt][c] == kNone ? 0.f : kUp - m[nt][c];
-            w[c] = ex2_approx(sc[s][nt][2 * h + c] + n);
-            l[nt][c] += w[c];
-            w[c] *= f;
-          }
-          const __half2 hi = __floats2half2_rn(w[0], w[1]);
-          const float2 b = __half22float2(hi);
+          const float x = w[s][nt][2 * h] * f, y = w[s][nt][2 * h + 1] * f;
+          const __half2 hi = __floats2half2_rn(x, y);
           ph[s][nt][h] = transpose8(*reinterpret_cast<const uint32_t*>(&hi));
-          pl[s][nt][h] = transpose8(half2_bits(w[0] - b.x, w[1] - b.y));
+          const float2 b = __half22float2(hi);
+          pl[s][nt][h] = transpose8(half2_bits(x - b.x, y - b.y));
         }
       }
     // ---- output
 #pragma unroll
-    for (int s = 0; s < G; ++s)
+    for (int s = 0; s < G; ++s) {
+      uint32_t vr[4][CW];           // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (D == 128) {
+          const uint4 v = ld_shared4(here + v_at + (j & 1) * 128 + (j >> 1) * 1024);
+          vr[j][0] = v.x;
+          vr[j][1] = v.y;
+          vr[j][2] = v.z;
+          vr[j][3] = v.w;
+        } else {
+          const uint2 v = ld_shared2(here + (j & 1 ? v_at ^ 64 : v_at) + s * 1024 + (j >> 1) * 512);
+          vr[j][0] = v.x;
+          vr[j][1] = v.y;
+        }
+      }
+      if (left < KB) {              // what is past the sequence may be NaN
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (16 * s + 2 * t + (j & 1) + 8 * (j >> 1) >= left)
+#pragma unroll
+            for (int w = 0; w < CW; ++w) vr[j][w] = 0u;
+      }
 #pragma unroll
       for (int w = 0; w < CW; ++w) {
-        const uint32_t* x = vr + s * 4 * CW + w;
         uint2 a[2], b[2];           // keys 2t, 2t + 1; keys 2t + 8, 2t + 9: columns 4w, 4w + 1, then 4w + 2, 4w + 3
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const uint32_t sel = y ? 0x7362 : 0x5140;
-          a[y] = decode4<kI8>(__byte_perm(x[0], x[CW], sel));
-          b[y] = decode4<kI8>(__byte_perm(x[2 * CW], x[3 * CW], sel));
+          a[y] = decode4<kI8>(__byte_perm(vr[0][w], vr[1][w], sel));
+          b[y] = decode4<kI8>(__byte_perm(vr[2][w], vr[3][w], sel));
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y)
@@ -389,19 +491,16 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
             mma8(o[nt][2 * w + y], a[y].x, a[y].y, b[y].x, b[y].y, pl[s][nt][0], pl[s][nt][1]);
           }
       }
-    if (lf < f1) {
-      load_v(ld);
-      if (++lf < f1) {
-        ld.advance(p, s_pre, per_seq);
-        read_pages(ld);
-      }
     }
+    __syncwarp();                   // the stage is read: the next issue may fill it
     // ---- the unit's end, or the share's
-    const bool last = cc.blk == cc.nb - 1;
-    if (last || f + 1 == f1) {
+    const bool last = left <= KB;
+    if (last || todo == 1) {
+      const int head = cc.unit / p.parts, part = cc.unit - head * p.parts;
+      const int have = min(kRows, p.group - part * kRows);
       const bool all = whole && last;
-      const long long piece = 2 * w_id + (f - cc.blk > f0 ? 1 : 0);   // as in the 16-bit kernel
-      const float unit = scale_of(E);
+      const long long piece = 2 * w_id + (later ? 1 : 0);   // as in the 16-bit kernel
+      const float unit = scale_of(E >> 23);
       const long long out0 = (static_cast<long long>(cc.i) * p.nh + head * p.group + part * kRows) * D;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -424,30 +523,33 @@ __global__ void __launch_bounds__(kLineWarps * 32, NT == 1 ? 2 : 1) attention_de
 #pragma unroll
             for (int e = 0; e < KS / 4; ++e) out[e] = p.bf16 ? pack16<__nv_bfloat16>(y + 8 * e) : pack16<__half>(y + 8 * e);
           } else {
-            if (g == 0) p.ml[piece * kRows + r] = make_float2(m[nt][c], sum);
+            if (g == 0) p.ml[piece * kRows + r] = make_float2(-n[nt][c], sum);
             float4* acc = reinterpret_cast<float4*>(p.acc + (piece * rows_kept + r) * D + 2 * KS * g);
 #pragma unroll
             for (int e = 0; e < KS / 2; ++e) acc[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           }
         }
     }
-    if (f + 1 < f1) {
-      const int u = cc.unit, i = cc.i;
-      cc.advance(p, s_pre, per_seq);
-      fresh = cc.unit != u || cc.i != i;
+    cc.left -= KB;
+    if (last && todo > 1) {
+      next_unit(cc);
+      fresh = whole = later = true;
     }
   }
 }
 
 template <bool kI8, int D, int NT>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {
-  const size_t smem = (static_cast<size_t>(p.n) + 1) * sizeof(long long);
-  const int ctas = decode8_ctas(p.group);
-  const cudaError_t e = launch_pdl(p.shift < 4 ? attention_decode8_kernel<kI8, D, NT, true> : attention_decode8_kernel<kI8, D, NT, false>,
-                                   dim3(ctas), dim3(kLineWarps * 32), smem, stream, p);
+  constexpr size_t kMost = ring8_bytes<NT>() + (kPrefixMax + 1) * sizeof(long long);
+  static SmemLimit limit;
+  const cudaError_t a = limit.raise(attention_decode8_kernel<kI8, D, NT>, kMost);
+  if (a != cudaSuccess) return a;
+  const size_t smem = ring8_bytes<NT>() + (p.n <= kPrefixMax ? (static_cast<size_t>(p.n) + 1) * sizeof(long long) : 0);
+  const cudaError_t e = launch_pdl(attention_decode8_kernel<kI8, D, NT>, dim3(num_sms()), dim3(Shape8<NT>::kWarps * 32), smem,
+                                   stream, p);
   if (e != cudaSuccess) return e;
-  return p.bf16 ? launch_join<__nv_bfloat16, D>(p, ctas * kLineWarps, stream)
-                : launch_join<__half, D>(p, ctas * kLineWarps, stream);
+  return p.bf16 ? launch_join<__nv_bfloat16, D>(p, decode8_warps(p.group), stream)
+                : launch_join<__half, D>(p, decode8_warps(p.group), stream);
 }
 template <bool kI8>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {

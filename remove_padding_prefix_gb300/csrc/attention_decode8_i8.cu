@@ -6,7 +6,7 @@ namespace rpp {
 cudaError_t launch_attention_decode8_e4m3(const void* params, cudaStream_t stream);   // attention_decode8_e4m3.cu
 
 size_t attention_decode8_ws_bytes(int n, int nh, int nkv, int d) {
-  return line_ws_bytes(n, nh, nkv, d, static_cast<long long>(decode8_ctas(nh / nkv)) * kLineWarps);
+  return line_ws_bytes(n, nh, nkv, d, decode8_warps(nh / nkv));
 }
 
 cudaError_t launch_attention_decode8(const KvDims& d, const KvState& c, const Kv8Scales& q8, int layer, const void* q,
@@ -19,6 +19,12 @@ cudaError_t launch_attention_decode8(const KvDims& d, const KvState& c, const Kv
   p.scales = q8.scales + heads * (d.page_size >> q8.shift);
   p.shift = q8.shift;
   p.bf16 = dtype == RPP_BF16;
+  p.head_bytes = static_cast<long long>(d.page_size) * d.head_dim;
+  p.v_bytes = d.kv_heads * p.head_bytes;
+  p.page_bytes = 2 * p.v_bytes;
+  p.head_scales = d.page_size >> q8.shift;
+  p.v_scales = d.kv_heads * p.head_scales;
+  p.page_scales = 2 * p.v_scales;
   p.table = c.table;
   p.lens = c.lens;
   p.q = q;
@@ -30,7 +36,7 @@ cudaError_t launch_attention_decode8(const KvDims& d, const KvState& c, const Kv
   p.parts = (p.group + kRows - 1) / kRows;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
-  line_ws_bind(&p, ws, static_cast<long long>(decode8_ctas(p.group)) * kLineWarps);
+  line_ws_bind(&p, ws, decode8_warps(p.group));
   p.err = err;
   return q8.i8 ? launch_codes<true>(p, stream) : launch_attention_decode8_e4m3(&p, stream);
 }

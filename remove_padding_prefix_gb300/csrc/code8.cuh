@@ -69,9 +69,9 @@ __device__ __forceinline__ uint2 decode4(uint32_t w) {
     r.x = *reinterpret_cast<const uint32_t*>(&a);
     r.y = *reinterpret_cast<const uint32_t*>(&b);
   } else {
-    const uint16_t lo = static_cast<uint16_t>(w), hi = static_cast<uint16_t>(w >> 16);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"(lo));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"(hi));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w));
   }
   return r;
 }

@@ -12,7 +12,6 @@ namespace rpp {
 
 namespace {
 
-constexpr int kLineWarps = 8;           // warps of a CTA of the main kernels
 constexpr int kMinBlocks = 2;           // blocks a warp takes at least, while there are that many
 constexpr int kRows = 16;               // query heads of a unit
 constexpr int kJoinThreads = 128;        // join by cuts
@@ -70,11 +69,11 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int i, int* slot) 
 
 // The first words of a main kernel: blocks of KB keys before each sequence in s_pre [n + 1] (and in p.prefix, for
 // the join), zeros for empty sequences.  Returns the blocks of one kv head part, -1 if the error word was set.
-// Holds __syncthreads: called by all threads.
-template <typename T, int D, int KB>
+// s_pre may be p.prefix itself: every CTA writes the same values.  Holds __syncthreads: called by all threads.
+template <typename T, int D, int KB, int W>
 __device__ __forceinline__ long long line_plan(const DecodeParams& p, long long* s_pre) {
   __shared__ int s_flag;
-  __shared__ long long s_warp[kLineWarps];
+  __shared__ long long s_warp[W];
   const int warp = warp_id(), lane = lane_id();
   // one reading of the error word for the whole CTA, on its way together with the first lengths
   if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
@@ -85,7 +84,7 @@ __device__ __forceinline__ long long line_plan(const DecodeParams& p, long long*
 
   // ---- blocks before each sequence
   long long carry = 0;
-  for (int base = 0; base < p.n; base += kLineWarps * 32) {
+  for (int base = 0; base < p.n; base += W * 32) {
     const int i = base + threadIdx.x;
     long long v = 0;
     if (i < p.n) {
@@ -101,7 +100,7 @@ __device__ __forceinline__ long long line_plan(const DecodeParams& p, long long*
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
     long long before = carry;
-    for (int w = 0; w < kLineWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < warp) before += s_warp[w];
       carry += s_warp[w];
     }
@@ -110,10 +109,10 @@ __device__ __forceinline__ long long line_plan(const DecodeParams& p, long long*
   }
   if (threadIdx.x == 0) s_pre[p.n] = carry;
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= p.n; i += kLineWarps * 32) p.prefix[i] = s_pre[i];
+  if (blockIdx.x == 0 && s_pre != p.prefix)
+    for (int i = threadIdx.x; i <= p.n; i += W * 32) p.prefix[i] = s_pre[i];
   // empty sequences: zeros
-  for (int i = warp * gridDim.x + blockIdx.x; i < p.n; i += kLineWarps * gridDim.x) {
+  for (int i = warp * gridDim.x + blockIdx.x; i < p.n; i += W * gridDim.x) {
     if (s_pre[i + 1] != s_pre[i]) continue;
     uint4* row = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<long long>(i) * p.nh * D);
     for (int e = lane; e < p.nh * (D / 8); e += 32) row[e] = make_uint4(0u, 0u, 0u, 0u);

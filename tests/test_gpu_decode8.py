@@ -3,7 +3,7 @@
 Tolerance, per output element, from the arithmetic (e = eps of the output type; V the sequence's values of that head,
 k its keys, n their number):
   * the final rounding: e / 2 of the value;
-  * a score is an fp32 sum of d exact products (a bf16 query's power of two loses at most 2^-38 of its largest element),
+  * a score is an fp32 sum of d exact products (a bf16 query's power of two loses at most 2^-32 of its largest element),
     scaled by two factors that are one rounding each: (d + 6) 2^-24 sum |q_c k_c|, and entering as
     exp(scale s) that, twice, times max |V|, on the weighted mean;
   * exp2 (2^-22), the base change of a score of magnitude z (2^-22 z), P kept to two f16 parts (2^-21), fp32 sums
