@@ -436,7 +436,13 @@ class KvCache:
     _calls |= {"decode": "rpp_attention_decode", "decode_workspace_bytes": "rpp_attention_decode_workspace_bytes"}
 
     def _call(self, name):
-        return getattr(lib(), self._calls[name])
+        """The C call, looked up once (a lookup costs a part of a launch)."""
+        fn = self._fns.get(name)
+        if fn is None:
+            fn = self._fns[name] = getattr(lib(), self._calls[name])
+        return fn
+
+    _fns = {}
 
     def _rows_dtype(self, dtype):
         """The type of rows that go in and come out, given one, and how the C calls take it."""
@@ -487,6 +493,8 @@ class KvCache8(KvCache):
 
     _calls = {name: call.replace("rpp_kv_", "rpp_kv8_").replace("decode", "decode8") for name, call in KvCache._calls.items()}
     _codes = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+    _fns = {}
+    _row_types = {torch.float16: (torch.float16, (RPP_F16,)), torch.bfloat16: (torch.bfloat16, (RPP_BF16,))}
 
     def __init__(self, layers, pages, page_size, kv_heads, head_dim, slots, max_pages, dtype="e4m3", block=16,
                  device="cuda"):
@@ -531,9 +539,10 @@ class KvCache8(KvCache):
             raise RppError("rpp_kv8_pool_bytes", _abi.RPP_EUNSUPPORTED)
 
     def _rows_dtype(self, dtype):
-        if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        got = self._row_types.get(dtype)
+        if got is None:
             raise ValueError(f"expected fp16 or bf16 rows, got {dtype}")
-        return dtype, (RPP_F16 if dtype is torch.float16 else RPP_BF16,)
+        return got
 
 
 def kv_reserve(cache: KvCache, slots, counts, err=None, stream=None):
@@ -589,9 +598,8 @@ def kv_read(cache: KvCache, layer: int, slots, cu_seqlens=None, starts=None, row
         elif isinstance(dtype, str):
             dtype = torch_dtype(dtype)
         dtype, code = cache._rows_dtype(dtype)
-        both = _made(stream, torch.empty, (rows, 2 * w), dtype=dtype, device=cache.pool.device)
-        k, v = both[:, :w], both[:, w:]
-        ld = 2 * w
+        k, v = (_made(stream, torch.empty, (rows, w), dtype=dtype, device=cache.pool.device) for _ in range(2))
+        ld = w
     else:
         rows = k.shape[0]
         dtype, code = cache._rows_dtype(k.dtype)

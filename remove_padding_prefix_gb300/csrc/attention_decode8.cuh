@@ -538,6 +538,18 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
   }
 }
 
+// The join: a CTA for each query head, of two warps while a unit has few pieces (on the average: the lengths are on the
+// device), else of eight.  64 sequences of 200 to 8192 keys, 32 heads on 8: 100 us with two, 103 by cuts; 48 with 32 heads on
+// 2: 34 and 68; 131000 keys of 16 heads: 61 with eight, 71 with two.
+template <typename T, int D>
+cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) {
+  constexpr int kFew = 64;
+  if (warps < 24LL * p.n * p.d.kv_heads * p.parts)
+    return launch_pdl(attention_decode_join_heads_kernel<T, D, kFew>, dim3(p.n, p.nh), dim3(kFew), 0, stream, p, warps);
+  return launch_pdl(attention_decode_join_heads_kernel<T, D, kHeadThreads>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream,
+                    p, warps);
+}
+
 template <bool kI8, int D, int NT>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {
   constexpr size_t kMost = ring8_bytes<NT>() + (kPrefixMax + 1) * sizeof(long long);
@@ -548,8 +560,8 @@ cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {
   const cudaError_t e = launch_pdl(attention_decode8_kernel<kI8, D, NT>, dim3(num_sms()), dim3(Shape8<NT>::kWarps * 32), smem,
                                    stream, p);
   if (e != cudaSuccess) return e;
-  return p.bf16 ? launch_join<__nv_bfloat16, D>(p, decode8_warps(p.group), stream)
-                : launch_join<__half, D>(p, decode8_warps(p.group), stream);
+  return p.bf16 ? launch_join8<__nv_bfloat16, D>(p, decode8_warps(p.group), stream)
+                : launch_join8<__half, D>(p, decode8_warps(p.group), stream);
 }
 template <bool kI8>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {

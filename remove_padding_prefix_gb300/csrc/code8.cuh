@@ -22,8 +22,8 @@ template <bool kI8> struct Code8 {
 __device__ __forceinline__ float scale_of(int b) {
   return b == 255 ? __int_as_float(0x7fffffff) : __int_as_float(b > 0 ? b << 23 : 1 << 22);
 }
-// 2^(127 - b) of a byte below 254
-__device__ __forceinline__ float inverse_of(int b) { return __int_as_float((254 - b) << 23); }
+// 2^(127 - b) of a byte below 255
+__device__ __forceinline__ float inverse_of(int b) { return __int_as_float(b < 254 ? (254 - b) << 23 : 1 << 22); }
 // 2^-n, 0 from n = 127 on (n >= 0)
 __device__ __forceinline__ float pow2_neg(int n) { return n < 127 ? __int_as_float((127 - n) << 23) : 0.f; }
 
@@ -48,10 +48,12 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     const uint32_t w = __float_as_uint(fminf(fmaxf(d, -kTop), kTop) + kMagic);
     return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
   } else {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
   }
 }
 

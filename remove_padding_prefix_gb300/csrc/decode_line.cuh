@@ -249,11 +249,11 @@ __global__ void __launch_bounds__(kJoinThreads, 12)
   }
 }
 
-// One CTA for each (sequence, query head): its warps share the pieces, a lane has D / 32 elements.
-template <typename T, int D>
-__global__ void __launch_bounds__(kHeadThreads)
+// One CTA of kThreads for each (sequence, query head): its warps share the pieces, a lane has D / 32 elements.
+template <typename T, int D, int kThreads>
+__global__ void __launch_bounds__(kThreads)
     attention_decode_join_heads_kernel(const DecodeParams p, int main_warps) {
-  constexpr int W = kHeadThreads / 32, E = D / 32;
+  constexpr int W = kThreads / 32, E = D / 32;
   __shared__ int s_flag;
   __shared__ float s_m[W], s_l[W];
   __shared__ float s_o[W][D];
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kHeadThreads)
   const long long first = 2 * w0 + (b0 > share_start(total, warps, w0) ? 1 : 0);
   auto piece = [&](int k) { return k ? 2 * (w0 + k) : first; };
   float mx = __int_as_float(0xff800000);
-  for (int k = threadIdx.x; k < pieces; k += kHeadThreads) mx = fmaxf(mx, p.ml[piece(k) * kRows + row].x);
+  for (int k = threadIdx.x; k < pieces; k += kThreads) mx = fmaxf(mx, p.ml[piece(k) * kRows + row].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) s_m[warp] = mx;
@@ -302,14 +302,14 @@ __global__ void __launch_bounds__(kHeadThreads)
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
   if (lane == 0) s_l[warp] = l;
   __syncthreads();
-  if (threadIdx.x < D) {
+  for (int c = threadIdx.x; c < D; c += kThreads) {
     float x = 0.f, z = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      x += s_o[w][threadIdx.x];
+      x += s_o[w][c];
       z += s_l[w];
     }
-    static_cast<T*>(p.out)[(static_cast<long long>(i) * p.nh + h) * D + threadIdx.x] = from_f32<T>(x / z);
+    static_cast<T*>(p.out)[(static_cast<long long>(i) * p.nh + h) * D + c] = from_f32<T>(x / z);
   }
 }
 
@@ -339,7 +339,7 @@ inline void line_ws_bind(DecodeParams* p, void* ws, long long warps) {
 template <typename T, int D>
 cudaError_t launch_join(const DecodeParams& p, int warps, cudaStream_t stream) {
   if (static_cast<long long>(p.n) * p.nh <= 4 * num_sms())
-    return launch_pdl(attention_decode_join_heads_kernel<T, D>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream, p, warps);
+    return launch_pdl(attention_decode_join_heads_kernel<T, D, kHeadThreads>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream, p, warps);
   return launch_pdl(attention_decode_join_cuts_kernel<T, D>, dim3(warps), dim3(kJoinThreads), 0, stream, p, warps);
 }
 
