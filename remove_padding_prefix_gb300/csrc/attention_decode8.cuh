@@ -89,7 +89,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 
 constexpr int kBlockBytes = 2048;                            // of K, and of V
 // Warps of a CTA (one an SM) and stages of a warp's ring: 16 warps of 128 registers while a unit has up to 8 query heads,
-// 8 of 255 for more; 192 KB of codes on their way to an SM, or in use, either way.
+// 8 of 255 for more (12 of 168: 38 us instead of 36 for the 48 sequences of launch_join8); 192 KB of codes on
+// their way to an SM, or in use, either way.
 template <int NT> struct Shape8 {
   static constexpr int kWarps = NT == 1 ? 16 : 8, kStages = NT == 1 ? 3 : 6;
 };
@@ -539,15 +540,15 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
 }
 
 // The join: a CTA for each query head, of two warps while a unit has few pieces (on the average: the lengths are on the
-// device), else of eight.  64 sequences of 200 to 8192 keys, 32 heads on 8: 100 us with two, 103 by cuts; 48 with 32 heads on
-// 2: 34 and 68; 131000 keys of 16 heads: 61 with eight, 71 with two.
+// device), else of sixteen.  64 sequences of 200 to 8192 keys, 32 heads on 8: 100 us with two, 103 by cuts; 48 with 32 heads on
+// 2: 34 and 68; 131000 keys of 16 heads: 54 with sixteen, 61 with eight, 71 with
+// two.
 template <typename T, int D>
 cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) {
-  constexpr int kFew = 64;
+  constexpr int kFew = 64, kMany = 512;
   if (warps < 24LL * p.n * p.d.kv_heads * p.parts)
     return launch_pdl(attention_decode_join_heads_kernel<T, D, kFew>, dim3(p.n, p.nh), dim3(kFew), 0, stream, p, warps);
-  return launch_pdl(attention_decode_join_heads_kernel<T, D, kHeadThreads>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream,
-                    p, warps);
+  return launch_pdl(attention_decode_join_heads_kernel<T, D, kMany>, dim3(p.n, p.nh), dim3(kMany), 0, stream, p, warps);
 }
 
 template <bool kI8, int D, int NT>
