@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
   const uint8_t *kp, *sp;           // of the unit to load, in page 0: this lane's chunk of K's first rows; its scale
   int at, row;                      // its next 16 keys: which of the sequence's pages, and the row in it
   int page[G], rows[G];             // of the block to load next
+  auto head_of = [&](int unit) { return p.parts == 1 ? unit : unit / p.parts; };
   auto enter_unit = [&]() {
-    const int head = ld.unit / p.parts;
+    const int head = head_of(ld.unit);
     kp = static_cast<const uint8_t*>(p.pool) + head * p.head_bytes + lr * D + lc * 16;
     sp = p.scales + static_cast<long long>(head) * p.head_scales + (lane < 16 ? 0 : p.v_scales);
     const int key = ld.len - ld.left;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
   bool fresh = true;
   for (; todo > 0; --todo) {
     if (fresh) {
-      const int head = cc.unit / p.parts, part = cc.unit - head * p.parts;
+      const int head = head_of(cc.unit), part = cc.unit - head * p.parts;
       const int have = min(kRows, p.group - part * kRows);
       fresh = false;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<long long>(cc.i) * p.q_stride +
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
     // ---- the unit's end, or the share's
     const bool last = left <= KB;
     if (last || todo == 1) {
-      const int head = cc.unit / p.parts, part = cc.unit - head * p.parts;
+      const int head = head_of(cc.unit), part = cc.unit - head * p.parts;
       const int have = min(kRows, p.group - part * kRows);
       const bool all = whole && last;
       const long long piece = 2 * w_id + (later ? 1 : 0);   // as in the 16-bit kernel
@@ -539,16 +540,77 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
   }
 }
 
-// The join: a CTA for each query head, of two warps while a unit has few pieces (on the average: the lengths are on the
-// device), else of sixteen.  64 sequences of 200 to 8192 keys, 32 heads on 8: 100 us with two, 103 by cuts; 48 with 32 heads on
-// 2: 34 and 68; 131000 keys of 16 heads: 54 with sixteen, 61 with eight, 71 with
-// two.
+// ---------------------------------------------------------------- join
+constexpr int kLongUnit = 8;         // pieces of a unit that are worth a CTA for each of its heads
+
+// The heads of all sequences whose units have about kLongUnit pieces or more, in the order of the sequences, CTA x of
+// `ctas` taking every ctas-th.
+template <typename T, int D>
+__device__ __forceinline__ void join_long_units(const DecodeParams& p, int main_warps, int x, int ctas) {
+  constexpr int W = kJoinThreads / 32;
+  __shared__ JoinShared<W, D> s;
+  __shared__ int s_seq[kJoinThreads], s_count[W];
+  const int warp = warp_id(), lane = lane_id();
+  const long long total = p.prefix[p.n] * (p.d.kv_heads * p.parts);
+  const long long warps = share_warps(total, main_warps);
+  auto is_long = [&](int i) {
+    return i < p.n && total > 0 && (p.prefix[i + 1] - p.prefix[i]) * warps >= kLongUnit * total;
+  };
+  bool any = false;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < p.n; i += kJoinThreads) any = any || is_long(i);
+  const int failed = __syncthreads_or(device_error_set(p.err));
+  if (!__syncthreads_or(any) || failed) return;
+  long long before = 0, next = x;    // long sequences passed; the head to take, counted over them
+  for (int base = 0; base < p.n; base += kJoinThreads) {
+    const int i = base + threadIdx.x;
+    const bool mine = is_long(i);
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) s_count[warp] = __popc(who);
+    __syncthreads();
+    int at = __popc(who & ((1u << lane) - 1u)), count = 0;
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) at += s_count[w];
+      count += s_count[w];
+    }
+    if (mine) s_seq[at] = i;
+    __syncthreads();
+    for (; next < (before + count) * p.nh; next += ctas) {
+      const int seq = s_seq[next / p.nh - before], h = static_cast<int>(next % p.nh);
+      const long long pre = p.prefix[seq], nb = p.prefix[seq + 1] - pre;
+      join_head<T, D, W>(p, seq, h, pre, nb, total, warps, s);
+      __syncthreads();               // s is used again
+    }
+    before += count;
+    __syncthreads();                 // s_seq and s_count are written again
+  }
+}
+
+// CTAs 0 .. main_warps - 1 have a cut each, those behind them the long units.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads, 8)
+    attention_decode8_join_kernel(const DecodeParams p, int main_warps) {
+  pdl_wait();
+  pdl_trigger();
+  if (static_cast<int>(blockIdx.x) < main_warps) join_cut<T, D, kLongUnit>(p, main_warps);
+  else join_long_units<T, D>(p, main_warps, blockIdx.x - main_warps, gridDim.x - main_warps);
+}
+
+// By query head where units have many pieces on the average (the lengths are on the device), with more warps the more pieces;
+// else by cuts, with CTAs for the heads of long units behind.  By cuts alone a sequence of 100000 keys among 600 of 20 to
+// 200 (32 heads on 8) takes 148 us, this way 96; among 100, 89 by heads and 73.  131000 keys of 16 heads: 54 us with
+// sixteen warps a head, 61 with eight; 48 sequences of 1000 to 6000, 32 heads on 2: 34 with four, 36 with eight, 42 by cuts.
 template <typename T, int D>
 cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) {
-  constexpr int kFew = 64, kMany = 512;
-  if (warps < 24LL * p.n * p.d.kv_heads * p.parts)
-    return launch_pdl(attention_decode_join_heads_kernel<T, D, kFew>, dim3(p.n, p.nh), dim3(kFew), 0, stream, p, warps);
-  return launch_pdl(attention_decode_join_heads_kernel<T, D, kMany>, dim3(p.n, p.nh), dim3(kMany), 0, stream, p, warps);
+  constexpr int kMany = 512, kSome = 128;
+  const long long units = static_cast<long long>(p.n) * p.d.kv_heads * p.parts;
+  if (warps >= 24 * units)
+    return launch_pdl(attention_decode_join_heads_kernel<T, D, kMany>, dim3(p.n, p.nh), dim3(kMany), 0, stream, p, warps);
+  if (warps >= kLongUnit * units)
+    return launch_pdl(attention_decode_join_heads_kernel<T, D, kSome>, dim3(p.n, p.nh), dim3(kSome), 0, stream, p, warps);
+  const long long heads = static_cast<long long>(p.n) * p.nh, most = 4 * num_sms();
+  return launch_pdl(attention_decode8_join_kernel<T, D>, dim3(warps + static_cast<int>(heads < most ? heads : most)),
+                    dim3(kJoinThreads), 0, stream, p, warps);
 }
 
 template <bool kI8, int D, int NT>

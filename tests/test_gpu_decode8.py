@@ -148,6 +148,19 @@ def test_many_short(n, hi, nh, nkv):
     check(got[-200:], q[-200:], c, 0, range(n - 200, n), nh)
 
 
+@pytest.mark.parametrize("n,nh,nkv,dtype", [(60, 8, 2, "bf16"), (300, 32, 8, "bf16"), (700, 16, 8, "fp16"), (200, 24, 1, "fp16")])
+def test_long_sequences_among_short_ones(n, nh, nkv, dtype):
+    """Units of many pieces and units of one or two joined by one call, the long ones at either end and in the middle."""
+    lens = [int(x) for x in np.random.default_rng(n).integers(0, 90, n)]
+    for i, m in ((0, 9000), (n // 2, 5000), (n // 2 + 1, 700), (n - 1, 12001)):
+        lens[i] = m
+    c = make("e4m3", lens, nkv, 128, 16, 16)
+    q = queries(n, nh, 128, dtype)
+    got = rpp.attention_decode(c, 0, q)
+    check(got, q, c, 0, range(n), nh)
+    assert torch.equal(rpp.attention_decode(c, 0, q), got)
+
+
 def test_nothing_to_attend_to():
     c = make("int8", [0, 0, 0], 4, 128, 16, 16)
     q = queries(3, 8, 128, "bf16")
