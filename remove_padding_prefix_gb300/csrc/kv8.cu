@@ -9,8 +9,8 @@
 // warp of a CTA finds where 16-row tiles (or blocks, if those are longer) and sequences begin among up to 32 packed
 // rows; then the warps share the tiles' heads: a warp looking on its own does that for every head again, a third of all
 // instructions with 8 heads (24 prompts, 16181 rows, d = 128: 26 us, this way 22.8).  A warp takes
-// one head's K or V of up to 16 rows (or one block, if that is longer): it holds the rows in registers, 16 bytes a lane
-// and row, reduces the magnitudes as 16-bit pairs (NaN largest), and writes codes and scale.  So the rows are read
+// one head's K or V (two of 64) of up to 16 rows (or one block, if that is longer): it holds the rows in registers, 16
+// bytes a lane and row, reduces the magnitudes as 16-bit pairs (NaN largest), and writes codes and scale.  So the rows are read
 // once; only blocks of 32 and more tokens take their rows from L2 a second time.  fp16 rows are turned into codes
 // as pairs where their scale is an f16 number, all others in fp32 (the same codes either way).
 // All rows of a block that a call brings are one warp's: no atomics, and results do not depend on timing.
@@ -165,25 +165,29 @@ struct Job {
   int has;                    // rows that its block has before it
 };
 
-// kFine: blocks of fewer than 16 tokens.  blockIdx.x: up to 32 packed rows (`tok`), grid-strided; blockIdx.y: spans of `span`
-// of the heads of K, then V.  The first warp finds where jobs begin among the rows, then the CTA's warps share
-// jobs times heads.  Dynamic shared memory: the list's offsets [n + 1], the slot bitmap.
-template <typename T, bool kI8, int D, bool kFine>
+// kFine: blocks of fewer than 16 tokens.  P: heads that a warp takes together, side by side in a row.  blockIdx.x: up to 32
+// packed rows (`tok`), grid-strided; blockIdx.y: spans of `span` times P of the heads of K, then V.  The first warp
+// finds where jobs begin among the rows, then the CTA's warps share jobs times heads.  Dynamic shared memory: the list's
+// offsets [n + 1], the slot bitmap.
+template <typename T, bool kI8, int D, int P, bool kFine>
 __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
     kv8_append_kernel(Codes c, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
                       const int32_t* __restrict__ refs, const T* __restrict__ k, const T* __restrict__ v, int row_stride,
                       const int32_t* __restrict__ slots, const int32_t* __restrict__ cu, int n, int rows_max, int tok,
                       int span, int32_t* err) {
-  constexpr int LPR = D / 8;            // lanes of a row
+  constexpr int GL = D / 8;             // lanes of a head's row
+  constexpr int LPR = P * GL;           // lanes of a row
   constexpr int RPS = 32 / LPR;         // rows of a step
   constexpr int S = 16 / RPS;           // steps of 16 rows
+  constexpr int kTwice = GL / S;        // lanes that end up with the same row's maximum (kFine): 1 or 2
+  static_assert((S == 4 || S == 8) && (kTwice == 1 || kTwice == 2), "steps and lanes of the reduction below");
   extern __shared__ int32_t s_list[];
   uint32_t* seen = reinterpret_cast<uint32_t*>(s_list + n + 1);
   __shared__ Gate gate;
   __shared__ Job s_job[kMaxTok];
   __shared__ int s_jobs;
   const int ps = c.d.page_size, heads = c.d.kv_heads;
-  const int kh0 = blockIdx.y * span, khs = min(span, 2 * heads - kh0);   // this CTA's heads
+  const int kh0 = blockIdx.y * span, khs = min(span, 2 * heads / P - kh0);   // this CTA's heads, P at a time
   pdl_wait();
   pdl_trigger();
   const int first = static_cast<int>(threadIdx.x) < n ? slots[threadIdx.x] : 0;
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
   const int head_scales = ps >> c.shift;
   const long long head_bytes = static_cast<long long>(ps) * D;
   const int warp = warp_id(), lane = lane_id();
-  const int lr = lane / LPR, lc = lane % LPR;
+  const int lr = lane / LPR, lc = lane % LPR, lg = lane % GL, lh = lc / GL;     // lh: which of the P heads
   // the warps side by side over the heads (K's, then V's), those that are left over the jobs
   const int wide = khs >= kMoveWarps ? kMoveWarps : khs >= 4 ? 4 : khs >= 2 ? 2 : 1, first_kh = kh0 + warp % wide;
   const int chunks = (T_rows + tok - 1) / tok;
@@ -251,13 +255,13 @@ __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
       const int has = x.has, o0 = x.at & (unit - 1), o1 = o0 + x.rows;   // the new rows' places among the unit's
       const int r0 = x.at - o0;                                       // the unit's place in the page
       const int b0 = o0 >> c.shift;                                   // the block that may have rows
-      const long long head = static_cast<long long>(x.page) * 2 * heads + first_kh;
+      const long long head = static_cast<long long>(x.page) * 2 * heads + first_kh * P + lh;
       uint8_t* codes = c.pool + head * head_bytes + r0 * D;
       uint8_t* scales = c.scales + head * head_scales + (r0 >> c.shift);
       const long long row0 = static_cast<long long>(x.t + lr - o0) * row_stride + lc * 8;   // the unit's row lr
-      for (int kh = first_kh; kh < kh0 + khs; kh += wide, codes += wide * head_bytes, scales += wide * head_scales) {
+      for (int kh = first_kh; kh < kh0 + khs; kh += wide, codes += wide * P * head_bytes, scales += wide * P * head_scales) {
         const int had = has ? scales[b0] : 0;
-        const T* src = (kh < heads ? k + kh * D : v + (kh - heads) * D) + row0;
+        const T* src = (kh * P < heads ? k + kh * P * D : v + (kh * P - heads) * D) + row0;
         uint4 w[S];
         auto load = [&](int base) {
           const T* a = src + static_cast<long long>(base) * row_stride;
@@ -280,10 +284,10 @@ __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
         int b = 0;                // a scale byte: kFine, of one row for each lane; else of the block
         bool fast;                // (the same in the whole warp)
         auto store = [&](int base) {
-          uint8_t* to = codes + (base + lr) * D + lc * 8;
+          uint8_t* to = codes + (base + lr) * D + lg * 8;
           int bs[S];              // of the rows that the lane stores
 #pragma unroll
-          for (int s = 0; s < S; ++s) bs[s] = kFine ? __shfl_sync(0xffffffffu, b, lr * LPR + s * 2) : b;
+          for (int s = 0; s < S; ++s) bs[s] = kFine ? __shfl_sync(0xffffffffu, b, lr * LPR + lh * GL + s * kTwice) : b;
           if (fast && base >= o0 && base + 16 <= o1) {
 #pragma unroll
             for (int s = 0; s < S; ++s) *reinterpret_cast<uint2*>(to + s * RPS * D) = encode8_fast<T, kI8>(w[s], bs[s]);
@@ -298,46 +302,46 @@ __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
         int lead_b;               // the scale byte of the block that may have rows
         int mine = 0;             // kFine: the lane's row
         if constexpr (kFine) {
-          // The rows' maxima, each in two lanes at the end: the lanes of a row group swap half of what they have with
-          // their neighbours 8, 4 and 2 on, so the row's step is in the lane's bits above the lowest.
+          // The rows' maxima, each in kTwice lanes at the end: the lanes of a head's row swap half of what they have with
+          // the lane GL / 2 on, then GL / 4 and so on, so the row's step is in the lane's upper bits.
           load(0);
           uint32_t z[S / 2];
 #pragma unroll
           for (int s = 0; s < S / 2; ++s) z[s] = either(most8<T>(w[s])) | either(most8<T>(w[s + S / 2])) << 16;
-          // z[s]: steps s (low) and s + S / 2 (high); first the halves, by the highest of the lane's step bits
-          {
-            const bool up = lc & (S == 8 ? 8 : 4);
+          {   // z[s]: steps s (low) and s + S / 2 (high)
+            const bool up = lg & (GL / 2);
 #pragma unroll
             for (int s = 0; s < S / 2; ++s) {
-              const uint32_t y = umax2(z[s], __shfl_xor_sync(0xffffffffu, z[s], S == 8 ? 8 : 4));
+              const uint32_t y = umax2(z[s], __shfl_xor_sync(0xffffffffu, z[s], GL / 2));
               z[s] = up ? y >> 16 : y & 0xffffu;
             }
           }
-          if constexpr (S == 8) {
-            const bool up = lc & 4;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint32_t give = up ? z[s] : z[s + 2], keep = up ? z[s + 2] : z[s];
-              z[s] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+          for (int n2 = S / 4, bit = GL / 4; n2 > 0; n2 >>= 1, bit >>= 1) {
+            const bool up = lg & bit;
+#pragma unroll
+            for (int s = 0; s < n2; ++s) {
+              const uint32_t give = up ? z[s] : z[s + n2], keep = up ? z[s + n2] : z[s];
+              z[s] = max(keep, __shfl_xor_sync(0xffffffffu, give, bit));
             }
           }
-          {
-            const bool up = lc & 2;
-            const uint32_t give = up ? z[0] : z[1], keep = up ? z[1] : z[0];
-            z[0] = max(keep, __shfl_xor_sync(0xffffffffu, give, 2));
-          }
-          z[0] = max(z[0], __shfl_xor_sync(0xffffffffu, z[0], 1));
-          mine = (lc >> 1) * RPS + lr;
-          // the rows of a block: a row's bits are lr's, then those of lc above the lowest
+          if constexpr (kTwice == 2) z[0] = max(z[0], __shfl_xor_sync(0xffffffffu, z[0], 1));
+          mine = lg / kTwice * RPS + lr;
+          // the rows of a block: a row's bits are lr's, then the lane's upper ones
 #pragma unroll
           for (int q = 1; q < 8; q <<= 1)
-            if (q < block) z[0] = max(z[0], __shfl_xor_sync(0xffffffffu, z[0], q < RPS ? q * LPR : q / RPS * 2));
+            if (q < block) z[0] = max(z[0], __shfl_xor_sync(0xffffffffu, z[0], q < RPS ? q * LPR : q / RPS * kTwice));
           const float most = of_bits<T>(z[0]);
           b = scale_byte<kI8>(most);
           const bool shares = has && (mine >> c.shift) == b0;
           if (shares) b = max(b, had);
           fast = __all_sync(0xffffffffu, mine < o0 || mine >= o1 || fast_ok<T, kI8>(most, b));
-          lead_b = has ? __reduce_max_sync(0xffffffffu, shares ? b : 0) : 0;
+          lead_b = shares ? b : 0;
+          if (has) {
+#pragma unroll
+            for (int q = 1; q < 32; q <<= 1)     // all lanes of the head
+              if (q < GL || q >= LPR) lead_b = max(lead_b, __shfl_xor_sync(0xffffffffu, lead_b, q));
+          }
         } else {
           const int first16 = o0 & ~15, last16 = (o1 - 1) & ~15;
           uint32_t m = 0;
@@ -346,31 +350,43 @@ __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
 #pragma unroll
             for (int s = 0; s < S; ++s) m = most2<T>(m, most8<T>(w[s]));
           }
-          m = __reduce_max_sync(0xffffffffu, either(m));
+          m = either(m);
+          if constexpr (P == 1) {
+            m = __reduce_max_sync(0xffffffffu, m);
+          } else {
+#pragma unroll
+            for (int q = 1; q < 32; q <<= 1)     // all lanes of the head
+              if (q < GL || q >= LPR) m = max(m, __shfl_xor_sync(0xffffffffu, m, q));
+          }
           const float most = of_bits<T>(m);
           b = lead_b = max(scale_byte<kI8>(most), had);
-          fast = fast_ok<T, kI8>(most, lead_b);
+          fast = __all_sync(0xffffffffu, fast_ok<T, kI8>(most, lead_b));
         }
-        if (has && lead_b > had && lead_b != 255) {       // (a byte of 255 stays for the block's life)
-          const float f = pow2_neg(lead_b - had);
-          uint4* old = reinterpret_cast<uint4*>(codes + (b0 << c.shift) * D);
-          const int vecs = has * (D / 16);
-          uint4 next = lane < vecs ? old[lane] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-          for (int e = lane; e < vecs; e += 32) {
-            uint4 z = next;
-            if (e + 32 < vecs) next = old[e + 32];
+        if (has && __any_sync(0xffffffffu, lead_b > had && lead_b != 255)) {       // (a byte of 255 stays for the block's life)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const float4 y = decode4f<kI8>((&z.x)[h]);
-              (&z.x)[h] = encode4<kI8>(y.x * f, y.y * f, y.z * f, y.w * f);
+          for (int e = 0; e < P; ++e) {          // one of the heads after the other
+            const int now = __shfl_sync(0xffffffffu, lead_b, e * GL), was = __shfl_sync(0xffffffffu, had, e * GL);
+            if (now <= was || now == 255) continue;
+            const float f = pow2_neg(now - was);
+            uint4* old = reinterpret_cast<uint4*>(codes + (e - lh) * head_bytes + (b0 << c.shift) * D);
+            const int vecs = has * (D / 16);
+            uint4 next = lane < vecs ? old[lane] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+            for (int i = lane; i < vecs; i += 32) {
+              uint4 z = next;
+              if (i + 32 < vecs) next = old[i + 32];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const float4 y = decode4f<kI8>((&z.x)[h]);
+                (&z.x)[h] = encode4<kI8>(y.x * f, y.y * f, y.z * f, y.w * f);
+              }
+              old[i] = z;
             }
-            old[e] = z;
           }
         }
         if constexpr (kFine) {
           store(0);
-          if (!(lc & 1) && mine >= o0 && mine < o1 && mine == max(o0, mine & ~(block - 1)))
+          if (lg % kTwice == 0 && mine >= o0 && mine < o1 && mine == max(o0, mine & ~(block - 1)))
             scales[mine >> c.shift] = static_cast<uint8_t>(b);
         } else {
           const int first16 = o0 & ~15, last16 = (o1 - 1) & ~15;
@@ -378,7 +394,7 @@ __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
             if (base != last16) load(base);
             store(base);
           }
-          if (lane == 0) scales[b0] = static_cast<uint8_t>(lead_b);
+          if (lr == 0 && lg == 0) scales[b0] = static_cast<uint8_t>(lead_b);
         }
       }
     }
@@ -525,7 +541,7 @@ struct AppendCall {
   cudaStream_t stream;
 };
 
-template <typename T, bool kI8, int D>
+template <typename T, bool kI8, int D, int P>
 cudaError_t append(const AppendCall& a) {
   const size_t smem = (static_cast<size_t>(a.n) + 1 + (a.c.d.slots + 31) / 32) * 4;
   // One wave of CTAs, with equal shares of the rows (up to 32 at a time); where there are fewer rows than that, CTAs share
@@ -533,11 +549,11 @@ cudaError_t append(const AppendCall& a) {
   const long long ctas = kAppendCtas * num_sms(), passes = (a.rows_max + ctas * kMaxTok - 1) / (ctas * kMaxTok);
   const int tok = static_cast<int>((a.rows_max + ctas * passes - 1) / (ctas * passes));
   const int x = blocks_for((static_cast<long long>(a.rows_max) + tok - 1) / tok, static_cast<int>(ctas));
-  const int khs = 2 * a.c.d.kv_heads, most = (khs + kMoveWarps - 1) / kMoveWarps, room = static_cast<int>(ctas / x);
+  const int khs = 2 * a.c.d.kv_heads / P, most = (khs + kMoveWarps - 1) / kMoveWarps, room = static_cast<int>(ctas / x);
   const int parts = most < room ? most : room;
   const int span = (khs + parts - 1) / parts;
   const dim3 grid(x, (khs + span - 1) / span);
-  return launch_pdl(a.c.shift < 4 ? kv8_append_kernel<T, kI8, D, true> : kv8_append_kernel<T, kI8, D, false>, grid,
+  return launch_pdl(a.c.shift < 4 ? kv8_append_kernel<T, kI8, D, P, true> : kv8_append_kernel<T, kI8, D, P, false>, grid,
                     dim3(kMoveThreads), smem, a.stream, a.c, static_cast<const int32_t*>(a.s->table),
                     static_cast<const int32_t*>(a.s->lens), static_cast<const int32_t*>(a.s->refs),
                     static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.row_stride, a.slots, a.cu, a.n, a.rows_max,
@@ -545,7 +561,11 @@ cudaError_t append(const AppendCall& a) {
 }
 template <typename T, bool kI8>
 cudaError_t append(const AppendCall& a) {
-  return a.c.d.head_dim == 64 ? append<T, kI8, 64>(a) : append<T, kI8, 128>(a);
+  if (a.c.d.head_dim == 128) return append<T, kI8, 128, 1>(a);
+  // Two heads of 64 at a time, once there are rows for every CTA: 23192 rows of 16 heads with a scale a token 31.6 us, one at
+  // a time 37.5; but one row of 12 heads 5.4 and 4.2.
+  const bool two = a.c.d.kv_heads % 2 == 0 && a.rows_max >= kAppendCtas * num_sms();
+  return two ? append<T, kI8, 64, 2>(a) : append<T, kI8, 64, 1>(a);
 }
 
 }  // namespace

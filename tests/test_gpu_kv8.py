@@ -233,6 +233,17 @@ def test_rows_read_back(shape, kind):
     p.check()
 
 
+@pytest.mark.parametrize("nkv,block,kind,dtype", [(2, 1, "int8", "fp16"), (2, 16, "e4m3", "bf16"), (4, 4, "e4m3", "fp16"),
+                                                  (3, 8, "int8", "bf16"), (2, 32, "int8", "fp16"), (2, 2, "int8", "bf16")])
+def test_more_rows_than_ctas(nkv, block, kind, dtype):
+    """Several thousand rows, twice, the second time into blocks that have some."""
+    p = Pair(1, 220, 32, nkv, 64, 12, 60, kind=kind, block=block, dtype=dtype)
+    p.grow([3, 0, 7, 5], [700, 1, 1801, 333])
+    p.check()
+    p.grow([0, 7, 3, 9], [900, 90, 801, 1000])
+    p.check()
+
+
 def test_one_row_each_without_cu_seqlens():
     p = Pair(2, 20, 16, 2, 64, 6, 5, kind="int8")
     slots = [4, 0, 2]
