@@ -599,9 +599,12 @@ RPP_API rpp_status rpp_attention_decode(const rpp_kv_cfg* cfg, const rpp_kv_cach
 /* ------------------------------------------------------------------------------
  * The same cache held in 8 bits: half the bytes of the pool, and of the attention over it.
  *
+ * Rows and queries are 16-bit (RPP_F16 or RPP_BF16, either with any cache).
+ *
  * The state is the 16-bit cache's but for the pool, int8 or e4m3 codes in the same layout, and one more array:
  *   scales  uint8[layers, pages, 2, kv_heads, page_size / block], 16-byte aligned; needs no initial contents
- * `block` tokens of a head share a scale byte b: a code c stands for c * 2^(b - 127), and b = 255 for NaN.  For the
+ * `block` tokens of a head share a scale byte b: a code c stands for c * 2^(b - 127), and b = 255 for NaN (a
+ * 16-bit row gives at most 248; rpp_attention_decode8 takes K's bytes of 254 for infinite).  For the
  * rows that rpp_kv8_append brings to a block, with a the largest magnitude among them,
  *   b = the smallest byte at which a is no more than half a step past the largest code (127 or 448), or the block's
  *       own, if it has rows already and that is larger;

@@ -597,7 +597,9 @@ def kv_read(cache: KvCache, layer: int, slots, cu_seqlens=None, starts=None, row
             dtype = torch.bfloat16 if isinstance(cache, KvCache8) else cache._dtype
         elif isinstance(dtype, str):
             dtype = torch_dtype(dtype)
-        dtype, code = cache._rows_dtype(dtype)
+        got, code = cache._rows_dtype(dtype)
+        if got is not dtype:
+            raise ValueError(f"dtype: a cache of {got} has no rows of {dtype}")
         k, v = (_made(stream, torch.empty, (rows, w), dtype=dtype, device=cache.pool.device) for _ in range(2))
         ld = w
     else:

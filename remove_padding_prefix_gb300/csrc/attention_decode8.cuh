@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
       const int other = __shfl_xor_sync(0xffffffffu, sc[s], 16);
       int x = lane < 16 ? sc[s] + 1 : other == 255 ? 255 : sc[s];
       if (16 * s + (lane & 15) >= sc_left) x = lane < 16 ? 253 : 0;
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc_to + s * 128), "r"(x << 23) : "memory");
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc_to + s * 128), "r"(static_cast<uint32_t>(x) << 23) : "memory");
     }
   };
 
@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
   float o[NT][KS][4];               // heads 2t, 2t + 1 of an even column, then of the odd one after it
   float l[NT][2];                   // sums of the weights 2^(score + n):
   float n[NT][2];                   // kUp - maximum; +inf before the first one, so that any score passes kMost
-  int E = 0;                        // output and weights are in units of 2^(e - 127), E = e << 23
+  int E = -1;                       // output and weights are in units of 2^(e - 127), E = e << 23; -1: no block yet, so that
+                                    // every unit's first block moves both E and n (weights with n = +inf may be NaN)
   bool fresh = true;
   for (; todo > 0; --todo) {
     if (fresh) {
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][k][e] = 0.f;
       }
-      E = 0;
+      E = -1;
     }
     cp_async_wait<kStages - 2>();
     __syncwarp();
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
     for (int s = 0; s < G; ++s)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float f = __int_as_float(max(vs[s][h] - E + (127 << 23), 0));
+        const float f = __int_as_float(max(static_cast<int>(static_cast<unsigned>(vs[s][h]) - E + (127u << 23)), 0));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float x = w[s][nt][2 * h] * f, y = w[s][nt][2 * h + 1] * f;

@@ -198,6 +198,23 @@ def check_wide(c, q, nh):
     check(rpp.attention_decode(c, 0, q), q, c, 0, range(q.shape[0]), nh)
 
 
+@pytest.mark.parametrize("d,nh,nkv", [(64, 4, 4), (128, 20, 1)])
+@pytest.mark.parametrize("zero", ["k", "v", "both"])
+def test_blocks_of_zeros(d, nh, nkv, zero):
+    """Zeros have the smallest scale there is, byte 0: values of 0 give 0, keys of 0 the values' mean."""
+    lens = [1, 2, 7, 8, 9, 15, 16, 17, 24, 33, 300]
+    c = make("e4m3", lens, nkv, d, 16, 16)
+    for kv in (0, 1):
+        if zero in ("kv"[kv], "both"):
+            c.pool.view(torch.uint8)[0, :, kv] = 0
+            c.scales[0, :, kv] = 0
+    q = queries(len(lens), nh, d, "fp16")
+    got = rpp.attention_decode(c, 0, q)
+    check(got, q, c, 0, range(len(lens)), nh)
+    if zero != "k":
+        assert (got == 0).all()
+
+
 @pytest.mark.parametrize("dtype,size", [("bf16", 2.0 ** 90), ("bf16", 2.0 ** -90), ("bf16", 2.0 ** -130), ("fp16", 60000.0),
                                         ("fp16", 2.0 ** -20)])
 def test_queries_of_any_size(dtype, size):

@@ -386,6 +386,9 @@ def test_arguments_of_the_binding():
         rpp.kv_read(c, 0, ints([0]), k=k)
     with pytest.raises(ValueError):
         rpp.kv_read(c, 0, ints([0]), dtype="fp32")
+    wide = rpp.KvCache(1, 4, 16, 2, 64, 2, 2, "bf16", dev())
+    with pytest.raises(ValueError):
+        rpp.kv_read(wide, 0, ints([0]), dtype="fp16")                 # it has bf16 rows
     with pytest.raises(ValueError):
         rpp.kv_read(c, 0, ints([0]), starts=ints([0, 1]))
     for bad in (c.scales[..., :0], c.scales.cpu(), c.scales.to(torch.int8), c.scales[:1], c.scales.transpose(0, 1)):
