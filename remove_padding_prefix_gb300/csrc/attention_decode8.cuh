@@ -544,12 +544,109 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
 // ---------------------------------------------------------------- join
 constexpr int kLongUnit = 8;         // pieces of a unit that are worth a CTA for each of its heads
 
+// One (sequence, query head) joined by the CTA's W warps, which share its pieces, in a fixed order; a lane has D / 32
+// elements.  One pass: a warp's maximum and sums come from the same readings, kDeep pieces on their way, the warps' meet in
+// shared memory.  pre, nb: the sequence's blocks in the line of one kv head part.
+template <int W, int D> struct JoinShared8 {
+  float m[W], l[W];
+  float o[W][D];
+};
+template <typename T, int D, int W>
+__device__ __forceinline__ void join_head8(const DecodeParams& p, int i, int h, long long pre, long long nb, long long total,
+                                           long long warps, JoinShared8<W, D>& s) {
+  constexpr int E = D / 32, kDeep = 4;
+  const int warp = warp_id(), lane = lane_id();
+  const float kNone = __int_as_float(0xff800000);
+  const int head = h / p.group, in_group = h - head * p.group;
+  const int part = in_group / kRows, row = in_group - part * kRows;
+  const long long b0 = pre * (p.d.kv_heads * p.parts) + (static_cast<long long>(head) * p.parts + part) * nb;
+  const long long w0 = share_of(total, warps, b0);
+  const int pieces = static_cast<int>(share_of(total, warps, b0 + nb - 1) - w0 + 1);
+  if (pieces == 1) return;                                          // written by the warp that had it
+  const int kept = p.group < kRows ? p.group : kRows;
+  const long long first = 2 * w0 + (b0 > share_start(total, warps, w0) ? 1 : 0);
+  float m = kNone, l = 0.f, acc[E] = {};
+  for (int k0 = warp; k0 < pieces; k0 += kDeep * W) {
+    float2 ml[kDeep];
+    float x[kDeep][E];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int k = k0 + u * W;
+      ml[u] = make_float2(kNone, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[u][e] = 0.f;
+      if (k < pieces) {
+        const long long piece = k ? 2 * (w0 + k) : first;
+        ml[u] = p.ml[piece * kRows + row];
+        const float* src = p.acc + (piece * kept + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[u][e] = src[e];
+      }
+    }
+    float to = m;
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) to = fmaxf(to, ml[u].x);
+    const float ref = to == kNone ? 0.f : to;                       // (no scores so far: 2^-inf, not 2^(-inf + inf))
+    const float a0 = ex2_approx(m - ref);
+    m = to;
+    l *= a0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = weighted(a0, acc[e]);
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const float a = ex2_approx(ml[u].x - ref);
+      l += a * ml[u].y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += weighted(a, x[u][e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s.o[warp][lane * E + e] = acc[e];
+  if (lane == 0) {
+    s.m[warp] = m;
+    s.l[warp] = l;
+  }
+  __syncthreads();
+  float top = kNone;
+#pragma unroll
+  for (int w = 0; w < W; ++w) top = fmaxf(top, s.m[w]);
+  const float ref = top == kNone ? 0.f : top;
+  for (int c = threadIdx.x; c < D; c += W * 32) {
+    float x = 0.f, z = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float a = ex2_approx(s.m[w] - ref);
+      x += weighted(a, s.o[w][c]);
+      z += a * s.l[w];
+    }
+    static_cast<T*>(p.out)[(static_cast<long long>(i) * p.nh + h) * D + c] = from_f32<T>(x / z);
+  }
+}
+
+// A CTA of kThreads for each (sequence, query head).
+template <typename T, int D, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+    attention_decode8_join_heads_kernel(const DecodeParams p, int main_warps) {
+  constexpr int W = kThreads / 32;
+  __shared__ int s_flag;
+  __shared__ JoinShared8<W, D> s;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
+  const int i = blockIdx.x, h = blockIdx.y;
+  const long long pre = p.prefix[i], nb = p.prefix[i + 1] - pre;
+  const long long total = p.prefix[p.n] * (p.d.kv_heads * p.parts);
+  __syncthreads();
+  if (s_flag || nb == 0) return;
+  join_head8<T, D, W>(p, i, h, pre, nb, total, share_warps(total, main_warps), s);
+}
+
 // The heads of all sequences whose units have about kLongUnit pieces or more, in the order of the sequences, CTA x of
 // `ctas` taking every ctas-th.
 template <typename T, int D>
 __device__ __forceinline__ void join_long_units(const DecodeParams& p, int main_warps, int x, int ctas) {
   constexpr int W = kJoinThreads / 32;
-  __shared__ JoinShared<W, D> s;
+  __shared__ JoinShared8<W, D> s;
   __shared__ int s_seq[kJoinThreads], s_count[W];
   const int warp = warp_id(), lane = lane_id();
   const long long total = p.prefix[p.n] * (p.d.kv_heads * p.parts);
@@ -579,7 +676,7 @@ __device__ __forceinline__ void join_long_units(const DecodeParams& p, int main_
     for (; next < (before + count) * p.nh; next += ctas) {
       const int seq = s_seq[next / p.nh - before], h = static_cast<int>(next % p.nh);
       const long long pre = p.prefix[seq], nb = p.prefix[seq + 1] - pre;
-      join_head<T, D, W>(p, seq, h, pre, nb, total, warps, s);
+      join_head8<T, D, W>(p, seq, h, pre, nb, total, warps, s);
       __syncthreads();               // s is used again
     }
     before += count;
@@ -606,9 +703,9 @@ cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) 
   constexpr int kMany = 512, kSome = 128;
   const long long units = static_cast<long long>(p.n) * p.d.kv_heads * p.parts;
   if (warps >= 24 * units)
-    return launch_pdl(attention_decode_join_heads_kernel<T, D, kMany>, dim3(p.n, p.nh), dim3(kMany), 0, stream, p, warps);
+    return launch_pdl(attention_decode8_join_heads_kernel<T, D, kMany>, dim3(p.n, p.nh), dim3(kMany), 0, stream, p, warps);
   if (warps >= kLongUnit * units)
-    return launch_pdl(attention_decode_join_heads_kernel<T, D, kSome>, dim3(p.n, p.nh), dim3(kSome), 0, stream, p, warps);
+    return launch_pdl(attention_decode8_join_heads_kernel<T, D, kSome>, dim3(p.n, p.nh), dim3(kSome), 0, stream, p, warps);
   const long long heads = static_cast<long long>(p.n) * p.nh, most = 4 * num_sms();
   return launch_pdl(attention_decode8_join_kernel<T, D>, dim3(warps + static_cast<int>(heads < most ? heads : most)),
                     dim3(kJoinThreads), 0, stream, p, warps);

@@ -248,18 +248,25 @@ __device__ __forceinline__ void join_cut(const DecodeParams& p, int main_warps) 
   }
 }
 
-// One (sequence, query head) joined by the CTA's W warps, which share its pieces; a lane has D / 32 elements.  pre, nb: the
-// sequence's blocks in the line of one kv head part.
-template <int W, int D> struct JoinShared {
-  float m[W], l[W];
-  float o[W][D];
-};
-template <typename T, int D, int W>
-__device__ __forceinline__ void join_head(const DecodeParams& p, int i, int h, long long pre, long long nb, long long total,
-                                          long long warps, JoinShared<W, D>& s) {
-  constexpr int E = D / 32;
-  const int warp = warp_id(), lane = lane_id();
+// One CTA for each (sequence, query head): its warps share the pieces, a lane has D / 32 elements.
+template <typename T, int D>
+__global__ void __launch_bounds__(kHeadThreads)
+    attention_decode_join_heads_kernel(const DecodeParams p, int main_warps) {
+  constexpr int W = kHeadThreads / 32, E = D / 32;
+  __shared__ int s_flag;
+  __shared__ float s_m[W], s_l[W];
+  __shared__ float s_o[W][D];
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
+  const int i = blockIdx.x, h = blockIdx.y;
+  const long long pre = p.prefix[i], nb = p.prefix[i + 1] - pre;
   const int per_seq = p.d.kv_heads * p.parts;
+  const long long total = p.prefix[p.n] * per_seq;
+  __syncthreads();
+  if (s_flag || nb == 0) return;
+  const int warp = warp_id(), lane = lane_id();
+  const long long warps = share_warps(total, main_warps);
   const int head = h / p.group, in_group = h - head * p.group;
   const int part = in_group / kRows, row = in_group - part * kRows;
   const long long b0 = pre * per_seq + (static_cast<long long>(head) * p.parts + part) * nb;   // the unit's first block
@@ -270,13 +277,13 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int i, int h, l
   const long long first = 2 * w0 + (b0 > share_start(total, warps, w0) ? 1 : 0);
   auto piece = [&](int k) { return k ? 2 * (w0 + k) : first; };
   float mx = __int_as_float(0xff800000);
-  for (int k = threadIdx.x; k < pieces; k += W * 32) mx = fmaxf(mx, p.ml[piece(k) * kRows + row].x);
+  for (int k = threadIdx.x; k < pieces; k += kHeadThreads) mx = fmaxf(mx, p.ml[piece(k) * kRows + row].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) s.m[warp] = mx;
+  if (lane == 0) s_m[warp] = mx;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < W; ++w) mx = fmaxf(mx, s.m[w]);
+  for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w]);
   const float m = mx == __int_as_float(0xff800000) ? 0.f : mx;
   float acc[E], l = 0.f;
 #pragma unroll
@@ -291,36 +298,18 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int i, int h, l
     for (int e = 0; e < E; ++e) acc[e] += weighted(a, src[e]);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) s.o[warp][lane * E + e] = acc[e];
-  if (lane == 0) s.l[warp] = l;
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+  if (lane == 0) s_l[warp] = l;
   __syncthreads();
-  for (int c = threadIdx.x; c < D; c += W * 32) {
+  if (threadIdx.x < D) {
     float x = 0.f, z = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      x += s.o[w][c];
-      z += s.l[w];
+      x += s_o[w][threadIdx.x];
+      z += s_l[w];
     }
-    static_cast<T*>(p.out)[(static_cast<long long>(i) * p.nh + h) * D + c] = from_f32<T>(x / z);
+    static_cast<T*>(p.out)[(static_cast<long long>(i) * p.nh + h) * D + threadIdx.x] = from_f32<T>(x / z);
   }
-}
-
-// One CTA of kThreads for each (sequence, query head).
-template <typename T, int D, int kThreads>
-__global__ void __launch_bounds__(kThreads)
-    attention_decode_join_heads_kernel(const DecodeParams p, int main_warps) {
-  constexpr int W = kThreads / 32;
-  __shared__ int s_flag;
-  __shared__ JoinShared<W, D> s;
-  pdl_wait();
-  pdl_trigger();
-  if (threadIdx.x == 0) s_flag = device_error_set(p.err) ? 1 : 0;
-  const int i = blockIdx.x, h = blockIdx.y;
-  const long long pre = p.prefix[i], nb = p.prefix[i + 1] - pre;
-  const long long total = p.prefix[p.n] * (p.d.kv_heads * p.parts);
-  __syncthreads();
-  if (s_flag || nb == 0) return;
-  join_head<T, D, W>(p, i, h, pre, nb, total, share_warps(total, main_warps), s);
 }
 
 template <typename T, int D>
@@ -357,7 +346,7 @@ inline void line_ws_bind(DecodeParams* p, void* ws, long long warps) {
 template <typename T, int D>
 cudaError_t launch_join(const DecodeParams& p, int warps, cudaStream_t stream) {
   if (static_cast<long long>(p.n) * p.nh <= 4 * num_sms())
-    return launch_pdl(attention_decode_join_heads_kernel<T, D, kHeadThreads>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream, p, warps);
+    return launch_pdl(attention_decode_join_heads_kernel<T, D>, dim3(p.n, p.nh), dim3(kHeadThreads), 0, stream, p, warps);
   return launch_pdl(attention_decode_join_cuts_kernel<T, D>, dim3(warps), dim3(kJoinThreads), 0, stream, p, warps);
 }
 
