@@ -7,7 +7,8 @@
 //
 //  * Work is cut as there (decode_line.cuh), in blocks of 2 KB of K and 2 KB of V.
 //  * Products are transposed: S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16, keys (or head columns) as the 16 rows and
-//    up to 8 query heads as the 8 columns, two such for 9 to 16.  The order of a contraction and the order of the
+//    up to 8 query heads as the 8 columns, two such for 9 to 16 (operands of tcgen05.mma would have to be written back to
+//    shared memory after their conversion, for results that come through tensor memory).  The order of a contraction and the order of the
 //    result's rows are free, so a lane's operands are 16 bytes of a row as they lie there: of K the columns 16 t .. of
 //    key rows g and g + 8 (Q's fragments take the same order), of V the columns 16 g .. of four keys, paired across
 //    keys by byte permutations (the output's rows take that order).
