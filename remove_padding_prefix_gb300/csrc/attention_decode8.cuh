@@ -13,7 +13,7 @@
 //    key rows g and g + 8 (Q's fragments take the same order), of V the columns 16 g .. of four keys, paired across
 //    keys by byte permutations (the output's rows take that order).
 //  * A warp keeps its own ring of blocks (cp.async, 16 bytes a lane), chunks moved inside their 128-byte line so that no
-//    reading meets a bank twice: 192 KB an SM on their way or in use.  Reading the cache straight into operand
+//    reading meets a bank twice: 64 to 147 KB an SM on their way or in use.  Reading the cache straight into operand
 //    registers, without the ring, leaves too few bytes on their way: 128 sequences of 200 to 8192 keys, d = 128, 32 heads
 //    on 8, e4m3: 238 us against 190; with blocks brought to L2 ahead of that by bulk prefetches: 275 and more.
 //  * Codes become f16 (exact for both types), so the products are exact in fp32.  fp16 queries are taken as they are; a bf16
@@ -89,22 +89,28 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 }
 
 constexpr int kBlockBytes = 2048;                            // of K, and of V
-// Warps of a CTA (one an SM) and stages of a warp's ring: 16 warps of 128 registers while a unit has up to 8 query heads,
-// 8 of 255 for more (12 of 168: 38 us instead of 36 for the 48 sequences of launch_join8); 192 KB of codes on
-// their way to an SM, or in use, either way.
-template <int NT> struct Shape8 {
-  static constexpr int kWarps = NT == 1 ? 16 : 8, kStages = NT == 1 ? 3 : 6;
+// Warps of a CTA (one an SM) and stages of a warp's ring.  Up to 8 query heads, d = 128: 12 and 3, 181 us for 128 sequences of
+// 200 to 8192 keys (e4m3); 16 and 3: 192, 16 and 2: 184, 12 and 4: 183, 12 and 2: 188.  d = 64 (twice the keys and
+// so the instructions for the same bytes): 16 and 2, 54.2 us for 131000 keys of 16 heads (int8); 16 and 3: 54.7, 12 and
+// 3: 56.8, 14 and 3: 58.5.  More than 8 heads: registers for 8 warps at d = 128 (3 stages 30.5 us, 6: 33 for 48 sequences of
+// 1000 to 6000 keys, 32 heads on 2; 12 warps that spill 33), 12 at d = 64 (192 sequences 56 us, with 8 warps 74).
+template <int D, int NT> struct Shape8 {
+  static constexpr int kWarps = NT == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
+  static constexpr int kStages = NT == 1 && D == 64 ? 2 : 3;
 };
 constexpr size_t kScaleBytes = 256;                          // of a stage: K's and V's of up to 32 keys, 4 bytes each
-template <int NT> constexpr size_t ring8_bytes() {
-  return Shape8<NT>::kWarps * Shape8<NT>::kStages * (2 * kBlockBytes + kScaleBytes);
+template <int D, int NT> constexpr size_t ring8_bytes() {
+  return Shape8<D, NT>::kWarps * Shape8<D, NT>::kStages * (2 * kBlockBytes + kScaleBytes);
 }
-constexpr int kPrefixMax = 2048;                             // longer lists keep their prefix in the workspace
-inline int decode8_warps(int group) { return num_sms() * (group <= 8 ? Shape8<1>::kWarps : Shape8<2>::kWarps); }
+inline int decode8_cta_warps(int group, int d) {
+  if (group <= 8) return d == 128 ? Shape8<128, 1>::kWarps : Shape8<64, 1>::kWarps;
+  return d == 128 ? Shape8<128, 2>::kWarps : Shape8<64, 2>::kWarps;
+}
+inline int decode8_warps(int group, int d) { return num_sms() * decode8_cta_warps(group, d); }
 
 template <bool kI8, int D, int NT>
-__global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_kernel(const Decode8Params p) {
-  constexpr int W = Shape8<NT>::kWarps, kStages = Shape8<NT>::kStages;
+__global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decode8_kernel(const Decode8Params p) {
+  constexpr int W = Shape8<D, NT>::kWarps, kStages = Shape8<D, NT>::kStages;
   constexpr int KB = kBlockBytes / D;            // keys of a block: 16 or 32
   constexpr int G = KB / 16;                     // groups of 16 keys
   constexpr int KS = D / 16;                     // k16 steps of the scores, and 16-row tiles of the output
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(Shape8<NT>::kWarps * 32, 1) attention_decode8_
   constexpr int kNaN = 255 << 23;
   const float kNone = __int_as_float(0xff800000);
   extern __shared__ __align__(1024) uint8_t smem[];
-  long long* s_pre = p.n <= kPrefixMax ? reinterpret_cast<long long*>(smem + ring8_bytes<NT>()) : p.prefix;   // [n + 1]
+  long long* s_pre = reinterpret_cast<long long*>(smem + ring8_bytes<D, NT>());   // [n + 1]
   const int warp = warp_id(), lane = lane_id();
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();
@@ -714,16 +720,16 @@ cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) 
 
 template <bool kI8, int D, int NT>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {
-  constexpr size_t kMost = ring8_bytes<NT>() + (kPrefixMax + 1) * sizeof(long long);
+  constexpr size_t kMost = ring8_bytes<D, NT>() + (kKvMaxList + 1) * sizeof(long long);
   static SmemLimit limit;
   const cudaError_t a = limit.raise(attention_decode8_kernel<kI8, D, NT>, kMost);
   if (a != cudaSuccess) return a;
-  const size_t smem = ring8_bytes<NT>() + (p.n <= kPrefixMax ? (static_cast<size_t>(p.n) + 1) * sizeof(long long) : 0);
-  const cudaError_t e = launch_pdl(attention_decode8_kernel<kI8, D, NT>, dim3(num_sms()), dim3(Shape8<NT>::kWarps * 32), smem,
+  const size_t smem = ring8_bytes<D, NT>() + (static_cast<size_t>(p.n) + 1) * sizeof(long long);
+  const cudaError_t e = launch_pdl(attention_decode8_kernel<kI8, D, NT>, dim3(num_sms()), dim3(Shape8<D, NT>::kWarps * 32), smem,
                                    stream, p);
   if (e != cudaSuccess) return e;
-  return p.bf16 ? launch_join8<__nv_bfloat16, D>(p, decode8_warps(p.group), stream)
-                : launch_join8<__half, D>(p, decode8_warps(p.group), stream);
+  return p.bf16 ? launch_join8<__nv_bfloat16, D>(p, decode8_warps(p.group, D), stream)
+                : launch_join8<__half, D>(p, decode8_warps(p.group, D), stream);
 }
 template <bool kI8>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {

@@ -6,7 +6,7 @@ namespace rpp {
 cudaError_t launch_attention_decode8_e4m3(const void* params, cudaStream_t stream);   // attention_decode8_e4m3.cu
 
 size_t attention_decode8_ws_bytes(int n, int nh, int nkv, int d) {
-  return line_ws_bytes(n, nh, nkv, d, decode8_warps(nh / nkv));
+  return line_ws_bytes(n, nh, nkv, d, decode8_warps(nh / nkv, d));
 }
 
 cudaError_t launch_attention_decode8(const KvDims& d, const KvState& c, const Kv8Scales& q8, int layer, const void* q,
@@ -36,7 +36,7 @@ cudaError_t launch_attention_decode8(const KvDims& d, const KvState& c, const Kv
   p.parts = (p.group + kRows - 1) / kRows;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
-  line_ws_bind(&p, ws, decode8_warps(p.group));
+  line_ws_bind(&p, ws, decode8_warps(p.group, d.head_dim));
   p.err = err;
   return q8.i8 ? launch_codes<true>(p, stream) : launch_attention_decode8_e4m3(&p, stream);
 }

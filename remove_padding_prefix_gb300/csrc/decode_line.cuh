@@ -69,7 +69,7 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int i, int* slot) 
 
 // The first words of a main kernel: blocks of KB keys before each sequence in s_pre [n + 1] (and in p.prefix, for
 // the join), zeros for empty sequences.  Returns the blocks of one kv head part, -1 if the error word was set.
-// s_pre may be p.prefix itself: every CTA writes the same values.  Holds __syncthreads: called by all threads.
+// Holds __syncthreads: called by all threads.
 template <typename T, int D, int KB, int W>
 __device__ __forceinline__ long long line_plan(const DecodeParams& p, long long* s_pre) {
   __shared__ int s_flag;
@@ -109,7 +109,7 @@ __device__ __forceinline__ long long line_plan(const DecodeParams& p, long long*
   }
   if (threadIdx.x == 0) s_pre[p.n] = carry;
   __syncthreads();
-  if (blockIdx.x == 0 && s_pre != p.prefix)
+  if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= p.n; i += W * 32) p.prefix[i] = s_pre[i];
   // empty sequences: zeros
   for (int i = warp * gridDim.x + blockIdx.x; i < p.n; i += W * gridDim.x) {
