@@ -561,7 +561,9 @@ template <int W, int D> struct JoinShared8 {
 template <typename T, int D, int W>
 __device__ __forceinline__ void join_head8(const DecodeParams& p, int i, int h, long long pre, long long nb, long long total,
                                            long long warps, JoinShared8<W, D>& s) {
-  constexpr int E = D / 32, kDeep = 4;
+  // with sixteen warps for long units 12 on their way (d = 64: 131000 keys of 16 heads 49.6 us, 4: 53.8) or 8 (d = 128: 30000
+  // keys, 32 heads on 8, 21.6, 4: 24.1); else 4 (8 sequences of 200 to 8192: 22.8, 8: 24.2)
+  constexpr int E = D / 32, kDeep = W < 16 ? 4 : D == 64 ? 12 : 8;
   const int warp = warp_id(), lane = lane_id();
   const float kNone = __int_as_float(0xff800000);
   const int head = h / p.group, in_group = h - head * p.group;
@@ -704,16 +706,17 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
 // By query head where units have many pieces on the average (the lengths are on the device), with more warps the more pieces;
 // else by cuts, with CTAs for the heads of long units behind.  By cuts alone a sequence of 100000 keys among 600 of 20 to
 // 200 (32 heads on 8) takes 148 us, this way 96; among 100, 89 by heads and 73.  131000 keys of 16 heads: 54 us with
-// sixteen warps a head, 61 with eight; 48 sequences of 1000 to 6000, 32 heads on 2: 34 with four, 36 with eight, 42 by cuts.
+// sixteen warps a head (before kDeep was 12), 61 with eight; 48 sequences of 1000 to 6000, 32 heads on 2: 34 with four, 36 with eight, 42 by cuts.
 template <typename T, int D>
 cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) {
   constexpr int kMany = 512, kSome = 128;
   const long long units = static_cast<long long>(p.n) * p.d.kv_heads * p.parts;
+  const long long heads = static_cast<long long>(p.n) * p.nh;
   if (warps >= 24 * units)
     return launch_pdl(attention_decode8_join_heads_kernel<T, D, kMany>, dim3(p.n, p.nh), dim3(kMany), 0, stream, p, warps);
   if (warps >= kLongUnit * units)
     return launch_pdl(attention_decode8_join_heads_kernel<T, D, kSome>, dim3(p.n, p.nh), dim3(kSome), 0, stream, p, warps);
-  const long long heads = static_cast<long long>(p.n) * p.nh, most = 4 * num_sms();
+  const long long most = 4 * num_sms();
   return launch_pdl(attention_decode8_join_kernel<T, D>, dim3(warps + static_cast<int>(heads < most ? heads : most)),
                     dim3(kJoinThreads), 0, stream, p, warps);
 }
