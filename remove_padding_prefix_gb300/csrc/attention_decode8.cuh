@@ -525,8 +525,9 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
           const float inv = 1.f / sum;
 #pragma unroll
           for (int e = 0; e < 2 * KS; ++e) {
-            y[e] = o[nt][e >> 1][2 * (e & 1) + c] * unit;
+            y[e] = o[nt][e >> 1][2 * (e & 1) + c];
             if (all) y[e] *= inv;
+            y[e] *= unit;
           }
           if (all) {
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out0 + r * D + 2 * KS * g);

@@ -229,6 +229,16 @@ def test_queries_of_any_size(dtype, size):
     check(rpp.attention_decode(c, 0, q), q, c, 0, range(2), 8)
 
 
+@pytest.mark.parametrize("lens", [[1, 16, 40] * 300, [3000, 900]])      # units whole in a warp, and cut ones
+@pytest.mark.parametrize("size", [87, -60])
+def test_values_of_any_size(lens, size):
+    """Values of up to 2^88 and tiny ones, bf16 outputs."""
+    c = make("int8", lens, 2, 64, 16, 16, spread=0)
+    c.scales[:, :, 1] = torch.where(c.scales[:, :, 1] == 255, 255, c.scales[:, :, 1].int() + size).to(torch.uint8)
+    q = queries(len(lens), 4, 64, "bf16")
+    check(rpp.attention_decode(c, 0, q), q, c, 0, range(len(lens)), 4)
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("d,nh,nkv,lens,block", [
     (64, 4, 4, [1, 2, 16, 17, 31, 40] * 40, 16), (128, 20, 1, [1, 2, 16, 17, 31, 40] * 40, 4), (128, 8, 2, [3000], 16),
