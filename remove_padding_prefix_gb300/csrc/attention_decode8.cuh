@@ -15,7 +15,7 @@
 //  * A warp keeps its own ring of blocks (cp.async, 16 bytes a lane), chunks moved inside their 128-byte line so that no
 //    reading meets a bank twice: 64 to 147 KB an SM on their way or in use.  Reading the cache straight into operand
 //    registers, without the ring, leaves too few bytes on their way: 128 sequences of 200 to 8192 keys, d = 128, 32 heads
-//    on 8, e4m3: 238 us against 190; with blocks brought to L2 ahead of that by bulk prefetches: 275 and more.
+//    on 8, e4m3: 238 us, with the ring then 190 (182 now); with blocks brought to L2 ahead by bulk prefetches 275 and more.
 //  * Codes become f16 (exact for both types), so the products are exact in fp32.  fp16 queries are taken as they are; a bf16
 //    query head is multiplied by the power of two that brings its largest element to 2^7 .. 2^8 (what that leaves below
 //    f16's smallest step is under 2^-31 of the largest) and its scores by the inverse.
@@ -25,8 +25,8 @@
 //    one's at the last move; so asks one vote a block, with whether V's scale moves, and the reductions over
 //    the lanes run only then.
 //  * P^T comes out of the scores' registers by two 8 x 8 transposes (movmatrix).  P is split into two f16
-//    parts (p and what rounding p left), as in the 16-bit kernel; that costs nothing in the batch above, and 2 us of 61 for
-//    131000 keys of 16 heads, int8, d = 64.
+//    parts (p and what rounding p left), as in the 16-bit kernel; that costs nothing in the batch above, and cost 2 us of 61
+//    for 131000 keys of 16 heads, int8, d = 64 (50 now).
 //
 // Codes past the sequence may be anything: their scores are -inf, their codes zeros.
 #pragma once
@@ -91,8 +91,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 constexpr int kBlockBytes = 2048;                            // of K, and of V
 // Warps of a CTA (one an SM) and stages of a warp's ring.  Up to 8 query heads, d = 128: 12 and 3, 181 us for 128 sequences of
 // 200 to 8192 keys (e4m3); 16 and 3: 192, 16 and 2: 184, 12 and 4: 183, 12 and 2: 188.  d = 64 (twice the keys and
-// so the instructions for the same bytes): 16 and 2, 54.2 us for 131000 keys of 16 heads (int8); 16 and 3: 54.7, 12 and
-// 3: 56.8, 14 and 3: 58.5.  More than 8 heads: registers for 8 warps at d = 128 (3 stages 30.5 us, 6: 33 for 48 sequences of
+// so the instructions for the same bytes): 16 and 2, 49.8 us for 131000 keys of 16 heads (int8); 12 and 3: 55.1, 14 and
+// 3: 55.0.  More than 8 heads: registers for 8 warps at d = 128 (3 stages 30.5 us, 6: 33 for 48 sequences of
 // 1000 to 6000 keys, 32 heads on 2; 12 warps that spill 33), 12 at d = 64 (192 sequences 56 us, with 8 warps 74).
 template <int D, int NT> struct Shape8 {
   static constexpr int kWarps = NT == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
@@ -705,9 +705,10 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
 }
 
 // By query head where units have many pieces on the average (the lengths are on the device), with more warps the more pieces;
-// else by cuts, with CTAs for the heads of long units behind.  By cuts alone a sequence of 100000 keys among 600 of 20 to
-// 200 (32 heads on 8) takes 148 us, this way 96; among 100, 89 by heads and 73.  131000 keys of 16 heads: 54 us with
-// sixteen warps a head (before kDeep was 12), 61 with eight; 48 sequences of 1000 to 6000, 32 heads on 2: 34 with four, 36 with eight, 42 by cuts.
+// else by cuts, with CTAs for the heads of long units behind.  By cuts alone, with no CTAs behind, a sequence of 100000 keys
+// among 600 of 20 to 200 (32 heads on 8) took 148 us, this way 94.  131000 keys of 16 heads: 50 us with sixteen warps a
+// head, 65 with four, 62 by cuts; 48 sequences of 1000 to 6000, 32 heads on 2: 31 with four, 48 with sixteen, 40 by cuts.
+// 128 of 200 to 8192, 32 heads on 8: 229 with sixteen, 182 by cuts.
 template <typename T, int D>
 cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) {
   constexpr int kMany = 512, kSome = 128;
@@ -725,6 +726,7 @@ cudaError_t launch_join8(const DecodeParams& p, int warps, cudaStream_t stream) 
 template <bool kI8, int D, int NT>
 cudaError_t launch_codes(const Decode8Params& p, cudaStream_t stream) {
   constexpr size_t kMost = ring8_bytes<D, NT>() + (kKvMaxList + 1) * sizeof(long long);
+  static_assert(kMost <= 227 * 1024);
   static SmemLimit limit;
   const cudaError_t a = limit.raise(attention_decode8_kernel<kI8, D, NT>, kMost);
   if (a != cudaSuccess) return a;
