@@ -21,9 +21,13 @@
 //    f16's smallest step is under 2^-31 of the largest) and its scores by the inverse.
 //  * K's scale multiplies the scores in fp32.  V's multiplies the weights, p 2^(vb - E) with E the largest vb so far,
 //    before they become f16 operands; E moves as the running maximum does, and 2^E multiplies the output at the end.
-//  * The maximum moves only when a lane's weights of a block (2 or 4 of a head) add up to more than 2^8 times the largest
+//  * The maximum moves only when a lane's weights of a block (2 or 4 of a head) add up to more than 2^7 times the largest
 //    one's at the last move; so asks one vote a block, with whether V's scale moves, and the reductions over
-//    the lanes run only then.
+//    the lanes run only then.  It moves by whole powers of two, so sums and outputs are rescaled exactly.
+//  * A score enters a weight as fma(s, c, n), n the maximum's counterpart as it is rounded.  The product in the fma is not,
+//    so weights are off by what rounding the maximum lost: nothing that matters below 2^16, but 32 powers of two at
+//    2^29.  From 2^16 on (and where 0 times an infinite c is NaN) the vote is for the other way, which takes a block's
+//    maximum first and rounds each product as it does there.  A score is infinite where it passes fp32's largest.
 //  * P^T comes out of the scores' registers by two 8 x 8 transposes (movmatrix).  P is split into two f16
 //    parts (p and what rounding p left), as in the 16-bit kernel; that costs nothing in the batch above, and cost 2 us of 61
 //    for 131000 keys of 16 heads, int8, d = 64 (50 now).
@@ -118,6 +122,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
   constexpr int CH = D / 16, RG = 32 / CH;       // 16-byte chunks of a row, rows that the lanes copy at once
   constexpr float kUp = 7.f;                     // weights (and their sum) are kept 2^7 times as large;
   constexpr float kMost = 32768.f;               // where a lane's of a block add up to more, the maximum moves
+  constexpr float kFar = 65536.f;                // a maximum this far from 0 needs rounded products
   constexpr int kNaN = 255 << 23;
   const float kNone = __int_as_float(0xff800000);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -257,10 +262,12 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
 
   const int rows_kept = p.group < kRows ? p.group : kRows;
   uint32_t qf[NT][KS][2];
-  float qs[NT][2];                  // scale (to base 2) of the scores of query heads 2t, 2t + 1, times 1/2
+  float qs[NT][2];                  // scale (to base 2) of the scores of query heads 2t, 2t + 1, times 1/2; where that is infinite
+                                    // minus 2^-128 times it
   float o[NT][KS][4];               // heads 2t, 2t + 1 of an even column, then of the odd one after it
   float l[NT][2];                   // sums of the weights 2^(score + n):
-  float n[NT][2];                   // kUp - maximum; +inf before the first one, so that any score passes kMost
+  float n[NT][2];                   // kUp - maximum, a whole number; +inf before the first one, so that any score passes kMost
+  bool careful = false;             // products are rounded on their own
   int E = -1;                       // output and weights are in units of 2^(e - 127), E = e << 23; -1: no block yet, so that
                                     // every unit's first block moves both E and n (weights with n = +inf may be NaN)
   bool fresh = true;
@@ -296,7 +303,8 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
           const int field = most >> 7;           // of the largest element; 255: no number, its head's output is NaN
           const int up = field == 255 ? 0 : min(7 + 127 - field, 110);   // (at 110 every bf16 is exact)
           const float f_up = __int_as_float((127 + up) << 23);
-          back *= __int_as_float((127 - up) << 23);
+          const float by = __int_as_float((127 - up) << 23);
+          back = back * by < __int_as_float(0x7f800000) ? back * by : -(back * 0x1p-64f * (by * 0x1p-64f));
 #pragma unroll
           for (int e = 0; e < 2 * KS; ++e)
             w[e] = half2_bits(__uint_as_float(w[e] << 16) * f_up, __uint_as_float(w[e] & 0xffff0000u) * f_up);
@@ -308,7 +316,8 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          qs[nt][c] = fmaxf(__shfl_sync(0xffffffffu, back, (2 * t + c) * 4), 1.4e-45f);
+          const float x = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
+          qs[nt][c] = x < 0.f ? x : fmaxf(x, 1.4e-45f);
           n[nt][c] = __int_as_float(0x7f800000);
           l[nt][c] = 0.f;
         }
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
     }
     // ---- weights
     float w[G][NT][4], sum[NT][2];
-    bool slow = false;
+    bool slow = careful;
     auto weigh = [&](int nt, int c) {
       sum[nt][c] = 0.f;
 #pragma unroll
@@ -396,7 +405,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         weigh(nt, c);
-        slow = slow || sum[nt][c] > kMost;
+        slow = slow || !(sum[nt][c] <= kMost);         // (or NaN)
       }
     if (__any_sync(0xffffffffu, slow)) {
       // the maximum or V's largest scale moves (or the unit has a block of NaN)
@@ -412,26 +421,48 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
       e1 = __reduce_max_sync(0xffffffffu, e1);
       const float ae = pow2_neg((e1 - E) >> 23), spoil = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
       E = e1;
+      careful = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float a[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          // the scores, one rounding each: powers of two that qs is kept short of come last (0 times what would be
+          // infinite is 0)
+          const bool huge = qs[nt][c] < 0.f, large = huge || qs[nt][c] > 1.f;
+          const float f = huge ? -qs[nt][c] : large ? qs[nt][c] * 0x1p-64f : qs[nt][c];
+          const float up = large ? 0x1p64f : 1.f, more = huge ? 0x1p64f : 1.f;
           float mx = kNone;
 #pragma unroll
           for (int s = 0; s < G; ++s)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, sc[s][nt][2 * h + c] * (ks[s][h] * qs[nt][c]));
+            for (int h = 0; h < 2; ++h) {
+              float& x = sc[s][nt][2 * h + c];
+              x = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(x, f), ks[s][h]), up), more);
+              mx = fmaxf(mx, x);
+            }
 #pragma unroll
           for (int x = 4; x <= 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
           a[c] = 1.f;
           if (mx + n[nt][c] > kUp + 6.f) {       // (not NaN: +inf on -inf)
-            a[c] = ex2_approx(kUp - mx - n[nt][c]);
-            n[nt][c] = kUp - mx;
+            const float to = ceilf(kUp - mx);
+            a[c] = ex2_approx(to - n[nt][c]);
+            n[nt][c] = to;
           }
+          const float by = n[nt][c] == -kNone ? 0.f : n[nt][c];        // (scores of -inf alone: weights of 0)
+          sum[nt][c] = 0.f;
+#pragma unroll
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              w[s][nt][2 * h + c] = ex2_approx(__fadd_rn(sc[s][nt][2 * h + c], by));
+              sum[nt][c] += w[s][nt][2 * h + c];
+            }
           l[nt][c] = fmaf(l[nt][c], a[c], spoil);
           a[c] *= ae;
-          weigh(nt, c);
+          const float all = l[nt][c] + sum[nt][c];
+          if (all != all) n[nt][c] = kNone;      // stays NaN, and holds up the others no more: all further weights are 0
+          else careful = careful || huge || fabsf(n[nt][c]) >= kFar;
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k)
