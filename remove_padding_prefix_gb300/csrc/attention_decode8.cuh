@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
   constexpr float kUp = 7.f;                     // weights (and their sum) are kept 2^7 times as large;
   constexpr float kMost = 32768.f;               // where a lane's of a block add up to more, the maximum moves
   constexpr float kFar = 65536.f;                // a maximum this far from 0 needs rounded products
+  constexpr float kStart = 3.402823466e38f;
   constexpr int kNaN = 255 << 23;
   const float kNone = __int_as_float(0xff800000);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -266,10 +267,11 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
                                     // minus 2^-128 times it
   float o[NT][KS][4];               // heads 2t, 2t + 1 of an even column, then of the odd one after it
   float l[NT][2];                   // sums of the weights 2^(score + n):
-  float n[NT][2];                   // kUp - maximum, a whole number; +inf before the first one, so that any score passes kMost
+  float n[NT][2];                   // kUp - maximum, a whole number; kStart before the first one, so that any score passes kMost
+  bool odd = false;                 // one of this lane's qs is not in [0, 1]
   bool careful = false;             // products are rounded on their own
   int E = -1;                       // output and weights are in units of 2^(e - 127), E = e << 23; -1: no block yet, so that
-                                    // every unit's first block moves both E and n (weights with n = +inf may be NaN)
+                                    // every unit's first block moves both E and n
   bool fresh = true;
   for (; todo > 0; --todo) {
     if (fresh) {
@@ -281,6 +283,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + g;
+        if (nt == 0) odd = false;
         uint32_t w[2 * KS];
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)
@@ -318,7 +321,8 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
         for (int c = 0; c < 2; ++c) {
           const float x = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
           qs[nt][c] = x < 0.f ? x : fmaxf(x, 1.4e-45f);
-          n[nt][c] = __int_as_float(0x7f800000);
+          n[nt][c] = kStart;
+          odd = odd || !(qs[nt][c] >= 0.f && qs[nt][c] <= 1.f);
           l[nt][c] = 0.f;
         }
 #pragma unroll
@@ -421,26 +425,37 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
       e1 = __reduce_max_sync(0xffffffffu, e1);
       const float ae = pow2_neg((e1 - E) >> 23), spoil = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
       E = e1;
-      careful = false;
+      // the scores, one rounding each
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float a[2];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          // the scores, one rounding each: powers of two that qs is kept short of come last (0 times what would be
-          // infinite is 0)
-          const bool huge = qs[nt][c] < 0.f, large = huge || qs[nt][c] > 1.f;
-          const float f = huge ? -qs[nt][c] : large ? qs[nt][c] * 0x1p-64f : qs[nt][c];
-          const float up = large ? 0x1p64f : 1.f, more = huge ? 0x1p64f : 1.f;
-          float mx = kNone;
+          float f = qs[nt][c], up = 1.f, more = 1.f;
+          if (odd) {                // powers of two kept for last: 0 times what would be infinite is 0
+            if (f < 0.f) more = 0x1p64f;
+            if (f < 0.f || f > 1.f) up = 0x1p64f;
+            f = f < 0.f ? -f : f > 1.f ? f * 0x1p-64f : f;
+          }
 #pragma unroll
           for (int s = 0; s < G; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = sc[s][nt][2 * h + c];
-              x = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(x, f), ks[s][h]), up), more);
-              mx = fmaxf(mx, x);
+              x = __fmul_rn(__fmul_rn(x, f), ks[s][h]);
+              if (odd) x = __fmul_rn(__fmul_rn(x, up), more);
             }
+        }
+      bool rare = odd;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float a[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = kNone;
+#pragma unroll
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, sc[s][nt][2 * h + c]);
 #pragma unroll
           for (int x = 4; x <= 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
           a[c] = 1.f;
@@ -449,25 +464,33 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
             a[c] = ex2_approx(to - n[nt][c]);
             n[nt][c] = to;
           }
-          const float by = n[nt][c] == -kNone ? 0.f : n[nt][c];        // (scores of -inf alone: weights of 0)
           sum[nt][c] = 0.f;
 #pragma unroll
           for (int s = 0; s < G; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              w[s][nt][2 * h + c] = ex2_approx(__fadd_rn(sc[s][nt][2 * h + c], by));
+              w[s][nt][2 * h + c] = ex2_approx(__fadd_rn(sc[s][nt][2 * h + c], n[nt][c]));
               sum[nt][c] += w[s][nt][2 * h + c];
             }
           l[nt][c] = fmaf(l[nt][c], a[c], spoil);
           a[c] *= ae;
-          const float all = l[nt][c] + sum[nt][c];
-          if (all != all) n[nt][c] = kNone;      // stays NaN, and holds up the others no more: all further weights are 0
-          else careful = careful || huge || fabsf(n[nt][c]) >= kFar;
+          rare = rare || !(fabsf(n[nt][c]) < kFar);
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][k][e] *= a[e & 1];
+      }
+      careful = false;
+      if (rare) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float all = l[nt][c] + sum[nt][c];
+            if (all != all) n[nt][c] = kNone;    // stays NaN, and holds up the others no more: further weights are 0
+            else careful = careful || qs[nt][c] < 0.f || fabsf(n[nt][c]) >= kFar;
+          }
       }
     }
     // ---- and their transposes as operands, in units of V's largest scale
