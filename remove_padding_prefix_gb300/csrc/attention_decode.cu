@@ -17,7 +17,8 @@
 //    16 rows: a tile of tcgen05.mma is 128 rows, eight times what there is, and its
 //    result would have to come back through tensor memory for each 8 KB.  The running
 //    maximum, the sum and the output stay in registers in fp32; the maximum moves only when
-//    it grows by more than 8 (log2 units).
+//    it grows by more than 8 (log2 units).  From maxima of 2^16 on the product of score and scale is
+//    rounded on its own, as the maximum's is: in an fma it is not, and from 2^29 on the two are up to 2^32 apart.
 //  * P is split into two 16-bit parts (p and what rounding p left), so the product with V
 //    keeps about 16 bits of P: the second mma costs nothing while HBM is the bound.
 //  * A (sequence, kv head) that one warp had whole is written at once.  Of one that was cut
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
   // fp16 weights (and so their sum and the output, too) are kept 2^7 times as large, up to 2^15: below the
   // smallest step of fp16, 2^-24, a weight is lost, and a long sequence has many small ones.
   constexpr float kUp = std::is_same<T, __half>::value ? 7.f : 0.f;
+  constexpr float kFar = 65536.f;                // a maximum this far from 0 needs rounded products
   extern __shared__ __align__(1024) uint8_t smem[];
   long long* s_pre = reinterpret_cast<long long*>(smem + kRingBytes);   // [n + 1]
   const int warp = warp_id(), lane = lane_id();
@@ -178,13 +180,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
   const int g = lane >> 2, t = lane & 3;
   uint32_t qf[KS][4];
   float o[D / 8][4];
-  float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+  float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, n[2] = {0.f, 0.f};
   const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;   // ldmatrix row / chunk of K
   const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;   // and of V
   const int rows_kept = p.group < kRows ? p.group : kRows;
   int stage = 0;
   bool fresh = true;                // the unit's first block in this share
   bool whole = false;               // that block is the unit's first
+  bool far = false;                 // one of the maxima is: scores are multiplied on their own,
+  float by = p.scale_log2;          // by 1 in the fma then
   for (long long f = f0; f < f1; ++f) {
     if (fresh) {
       fresh = false;
@@ -206,7 +210,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
       m[0] = m[1] = __int_as_float(0xff800000);
-      l[0] = l[1] = 0.f;
+      l[0] = l[1] = n[0] = n[1] = 0.f;
+      far = false;
+      by = p.scale_log2;
     }
     cp_async_wait<kStages - 2>();
     __syncwarp();
@@ -261,8 +267,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
     }
     mx[0] *= p.scale_log2;
     mx[1] *= p.scale_log2;
-    const bool move0 = mx[0] > m[0] + 8.f, move1 = mx[1] > m[1] + 8.f;
-    if (__any_sync(0xffffffffu, move0 || move1)) {
+    // (rounded down, so that no weight passes 2^15)
+    const bool move0 = mx[0] > __fadd_rd(m[0], 8.f), move1 = mx[1] > __fadd_rd(m[1], 8.f);
+    if (__any_sync(0xffffffffu, move0 || move1 || far)) {
       const float a0 = move0 ? ex2_approx(m[0] - mx[0]) : 1.f, a1 = move1 ? ex2_approx(m[1] - mx[1]) : 1.f;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
@@ -275,15 +282,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
       l[1] *= a1;
       if (move0) m[0] = mx[0];
       if (move1) m[1] = mx[1];
+      bool away = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // a row whose scores so far are all -inf keeps m = -inf: its P is 0, not 2^(-inf + inf)
+        if (m[e] == __int_as_float(0xff800000)) continue;
+        n[e] = fabsf(m[e]) < kFar ? kUp - m[e] : __fsub_rd(kUp, m[e]);
+        away = away || !(fabsf(m[e]) < kFar);
+      }
+      far = __any_sync(0xffffffffu, away);
+      by = far ? 1.f : p.scale_log2;
+      if (far)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = __fmul_rn(s[j][e], p.scale_log2);
     }
-    // a row whose scores so far are all -inf keeps m = -inf: its P is 0, not 2^(-inf + inf)
-    const float n0 = m[0] == __int_as_float(0xff800000) ? 0.f : kUp - m[0];
-    const float n1 = m[1] == __int_as_float(0xff800000) ? 0.f : kUp - m[1];
     uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const float p00 = ex2_approx(fmaf(s[j][0], p.scale_log2, n0)), p01 = ex2_approx(fmaf(s[j][1], p.scale_log2, n0));
-      const float p10 = ex2_approx(fmaf(s[j][2], p.scale_log2, n1)), p11 = ex2_approx(fmaf(s[j][3], p.scale_log2, n1));
+      const float p00 = ex2_approx(fmaf(s[j][0], by, n[0])), p01 = ex2_approx(fmaf(s[j][1], by, n[0]));
+      const float p10 = ex2_approx(fmaf(s[j][2], by, n[1])), p11 = ex2_approx(fmaf(s[j][3], by, n[1]));
       l[0] += p00 + p01;
       l[1] += p10 + p11;
       split2<T>(p00, p01, &ph[j][0], &pl[j][0]);

@@ -1,10 +1,10 @@
-"""Attention of one new token over the 8-bit cache where numbers leave the usual range: scores up to fp32's largest, a
+"""Attention of one new token over either cache where numbers leave the usual range: scores up to fp32's largest, a
 large `scale` beside scores of zero.  Against fp64.
 
 Tolerances (e = eps of the output type).  Scores, one key ahead of all others by far more than scores of that size are
 rounded: its weight alone is above 0, whatever that rounding was, so the output is its value, off by
   * the final rounding, e / 2 of it;
-  * exp2, 2^-22, of the weight and of the factors of a join (at most two), P in two 16-bit parts (2^-21),
+  * exp2, 2^-22, of the weight and of the factors of a join (at most two), P in two 16-bit parts (2^-21 in f16, 2^-17 in bf16),
     the products, sum, quotient and unit after it (eight roundings of 2^-24) and as many in a join;
   * fp16's smallest values, 2^-25, and half a step of f16's smallest where the weight is 2^6 at least, 2^-31 of the largest
     code's value.
@@ -13,6 +13,7 @@ import pytest
 import torch
 
 import remove_padding_prefix_gb300 as rpp
+import test_gpu_decode as t16
 import test_gpu_decode8 as t8
 from gpu_util import TDT, dev
 from test_gpu_decode8 import EPS, TOP
@@ -87,6 +88,36 @@ def test_scores_of_any_size_over_codes(kind, dtype, d, nh, nkv, lens, sign, by):
         q_up = 0 if by == "scale" else up - k_up
         scale = 1.37 * 2.0 ** (up if by == "scale" else 0)
         c.scales[0, :, 0] = torch.where(used, 127 - 7 + k_up, 255).to(torch.uint8)
+        q = along(len(lens), u, nh // nkv, dtype, 2.0 ** q_up)
+        got = rpp.attention_decode(c, 0, q, scale=scale)
+        assert rpp.get_device_error(c.err) == 0
+        close(got, want, EPS[dtype], rest)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,nh,nkv", HEADS)
+@pytest.mark.parametrize("lens", [WHOLE, CUT], ids=["whole", "cut"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("by", ["scale", "rows"])
+def test_scores_of_any_size_over_16_bits(dtype, d, nh, nkv, lens, sign, by):
+    if by == "rows" and dtype == "fp16":
+        pytest.skip("fp16 rows reach scores of 2^38, with the scale of the other case")
+    c = t16.make(dtype, lens, nkv, d, 16)
+    rows, top, u = ahead(lens, nkv, d, sign)
+    want = []
+    for s, n in enumerate(lens):
+        want.append(t16.sequence(c, 0, s)[1][top[s]].repeat_interleave(nh // nkv, 0).flatten())
+    want = torch.stack(want)
+    part = 2.0 ** -21 if dtype == "fp16" else 2.0 ** -17
+    rest = want.abs().max() * (2 * 3 * 2.0 ** -22 + part + 16 * 2.0 ** -24) + 2.0 ** -31
+    for z in (20, 24, 25, 26, 28, 30, 31, 33, 40, 60, 110):
+        up = z - 6
+        k_up = 0 if by == "scale" else up // 2
+        q_up = 0 if by == "scale" else up - k_up
+        scale = 1.37 * 2.0 ** (up if by == "scale" else 0)
+        for s in range(len(lens)):
+            page, row = places(c, s)
+            c.pool[0, page, 0, :, row] = (rows[s].double() * 2.0 ** (k_up - 7)).to(TDT[dtype])
         q = along(len(lens), u, nh // nkv, dtype, 2.0 ** q_up)
         got = rpp.attention_decode(c, 0, q, scale=scale)
         assert rpp.get_device_error(c.err) == 0
