@@ -565,7 +565,8 @@ RPP_API rpp_status rpp_kv_read(const rpp_kv_cfg* cfg, const rpp_kv_cache* cache,
  * gives what the formula does, a weight being above 0, however small, but for a score of -inf.
  * The weights are rounded to dtype for their product with v (their sum is not), off by up to 2^-8 (bf16)
  * or 2^-11 (fp16) of each; sums are fp32 before the division, of weights up to 2^8: bf16 values above
- * 2^100 may overflow them.
+ * 2^100 may overflow them.  Scores are fp32, one beyond 2^127 may count as infinite; weights beside the largest
+ * of a row are within what rounding scores of their size to fp32 leaves open.
  *  q       device rows of nh * d of dtype, q_stride elements apart; k, v: rows of nkv * d,
  *          kv_stride apart (strides are multiples of 8, so the three may be columns of a
  *          QKV projection's output); T_max <= 2^31 - 65536 rows each

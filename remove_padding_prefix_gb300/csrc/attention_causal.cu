@@ -611,10 +611,17 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
     const int quad = warp & 3;                     // tensor-memory lanes of this warp
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t t_p = t_s + S::kColP, t_o = t_s + S::kColO;
-    const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
+    // a power of two from it on (2^127 at most)
+    const float scale_up = __int_as_float(min((__float_as_int(scale_log2) + 0x7fffff) & 0x7f800000, 254 << 23));
     // fp16 weights (and so their sum and O) are kept 2^7 times as large, up to 2^15: below the smallest
     // step of fp16, 2^-24, a weight is lost, and a long sequence has many small ones.
     constexpr float kUp = std::is_same<T, __half>::value ? 7.f : 0.f;
+    // A maximum is a rounded product, the weights' exponents come from an fma, whose product is not: they differ by up to
+    // half a last place of the maximum, and that has to stay inside the weights' range.  From kFar on weights begin
+    // lower and the maximum moves with every larger score; from kOne on two scores that differ are 16 or more apart, so
+    // beside the largest one weights are below 2^-16 whatever the scale, and a scale that is a power of two (the
+    // next one) makes the products exact.  Tests of scores of any size; 1.2% of the time of long prompts.
+    constexpr float kFar = 0x1p22f, kOne = 0x1p28f;
     uint8_t* stage = smem + S::kOffStage + (4 * xs + quad) * 2048;
     uint32_t ns = 0, no = 0;
     bool ok = true;
@@ -643,7 +650,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
           break;
         }
         tc_fence_after();
-        uint64_t sum2[2] = {0ull, 0ull}, nm2 = 0ull;
+        uint64_t sum2[2] = {0ull, 0ull}, nm2 = 0ull, by2 = 0ull;
         // the last PV has read P and left O (P over S: s_full says so)
         auto last_pv = [&]() -> bool {
           if (!S::kApart || j == 0) return true;
@@ -653,8 +660,9 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
         };
         // Takes the tile's maximum into the row's: it moves lazily, and then O and the sum with it.
         // The accesses to tensor memory are the whole warp's (factor 1 for the rows that stay).
-        auto take_max = [&](float mx) {
-          const bool move = mx > m + 8.0f;
+        auto take_max = [&](float top) {
+          const float mx = __fmul_rn(top, scale_log2);
+          const bool move = mx > (fabsf(m) < kFar ? m + 8.0f : m);
           if (j == 0) {
             m = mx;
           } else if (__any_sync(0xffffffffu, move)) {
@@ -675,13 +683,21 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
             }
           }
           // scores all -inf so far: weights 0, not 2^(-inf + inf)
-          const float nm = m == neg_inf() ? 0.f : kUp - m;
+          float nm = m == neg_inf() ? 0.f : kUp - m, by = scale_log2;
+          if (fabsf(m) >= kFar && m != neg_inf()) {
+            nm = (kUp > 0.f ? 4.f : 0.f) - m;
+            if (fabsf(m) >= kOne) {
+              by = scale_up;
+              nm = mx < m ? neg_inf() : -top * by;
+            }
+          }
           nm2 = f2_pack(nm, nm);
+          by2 = f2_pack(by, by);
         };
         auto weights = [&](const uint32_t* sc, uint32_t* p, int n2) {   // 2 n2 scores -> n2 pairs of weights
 #pragma unroll
           for (int e = 0; e < n2; ++e) {
-            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), sc2, nm2);
+            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), by2, nm2);
             const float p0 = ex2_approx(f2_lo(x2)), p1 = ex2_approx(f2_hi(x2));
             sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
             p[e] = pack2<T>(p0, p1);
@@ -728,7 +744,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
             ok = false;
             break;
           }
-          take_max(fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]) * scale_log2);
+          take_max(fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]));
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             weights(v + 64 * c, v + 32 * c, 32);
@@ -767,7 +783,7 @@ __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
             ok = false;
             break;
           }
-          if (seen > 0) take_max(mx * scale_log2);
+          if (seen > 0) take_max(mx);
 #pragma unroll 1
           for (int c = 0; c < kT / 32; ++c) {
             if (c < seen) {
