@@ -19,11 +19,14 @@
 //  * Codes become f16 (exact for both types), so the products are exact in fp32.  fp16 queries are taken as they are; a bf16
 //    query head is multiplied by the power of two that brings its largest element to 2^7 .. 2^8 (what that leaves below
 //    f16's smallest step is under 2^-31 of the largest) and its scores by the inverse.
-//  * K's scale multiplies the scores in fp32.  V's multiplies the weights, p 2^(vb - E) with E the largest vb so far,
-//    before they become f16 operands; E moves as the running maximum does, and 2^E multiplies the output at the end.
-//  * The maximum moves only when a lane's weights of a block (2 or 4 of a head) add up to more than 2^7 times the largest
-//    one's at the last move; so asks one vote a block, with whether V's scale moves, and the reductions over
-//    the lanes run only then.  It moves by whole powers of two, so sums and outputs are rescaled exactly.
+//  * K's scale multiplies the scores in fp32.  V's multiplies the weights before they become f16 operands, p 2^(vb - E), an
+//    addition to p's exponent; 2^E multiplies the output at the end.  E is a query head's own and follows its largest
+//    p 2^vb: by the largest vb alone, a block that no query looks at would push those that carry the output out of f16's
+//    range (bytes 45 apart: 0).
+//  * At a unit's first block the largest weight, and the largest in units of 2^E, become 2^7 to 2^8.  E moves when one
+//    passes f16's largest, the maximum then, or when a lane's weights of a block (2 or 4 of a head) add up to more than 2^40:
+//    so asks one vote a block, and the reductions over the lanes run only then.  Both move by whole powers of two, so sums
+//    and outputs are rescaled exactly.  E of its own for each head costs 0.2 to 2% where HBM is the bound, 3 to 5% with 9 to 16 heads.
 //  * A score enters a weight as fma(s, c, n), n the maximum's counterpart as it is rounded.  The product in the fma is not,
 //    so weights are off by what rounding the maximum lost: nothing that matters below 2^16, but 32 powers of two at
 //    2^29.  From 2^16 on (and where 0 times an infinite c is NaN) the vote is for the other way, which takes a block's
@@ -121,8 +124,10 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
   constexpr int CW = D / 32;                     // words of V that a lane has of a key
   constexpr int CH = D / 16, RG = 32 / CH;       // 16-byte chunks of a row, rows that the lanes copy at once
   constexpr float kUp = 7.f;                     // weights (and their sum) are kept 2^7 times as large;
-  constexpr float kMost = 32768.f;               // where a lane's of a block add up to more, the maximum moves
+  constexpr float kMost = 0x1p40f;               // where a lane's of a block add up to more, the maximum moves
   constexpr float kFar = 65536.f;                // a maximum this far from 0 needs rounded products
+  constexpr int kTop = 0x477fe000;               // 65504.f: where a weight in units of 2^E is above it, E moves
+  constexpr int kApart = 64 << 23;               // where V's scale is further above E than this, exponents may not be added blindly
   constexpr float kStart = 3.402823466e38f;
   constexpr int kNaN = 255 << 23;
   const float kNone = __int_as_float(0xff800000);
@@ -270,8 +275,9 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
   float n[NT][2];                   // kUp - maximum, a whole number; kStart before the first one, so that any score passes kMost
   bool odd = false;                 // one of this lane's qs is not in [0, 1]
   bool careful = false;             // products are rounded on their own
-  int E = -1;                       // output and weights are in units of 2^(e - 127), E = e << 23; -1: no block yet, so that
-                                    // every unit's first block moves both E and n
+  int E[NT][2];                     // outputs and weights are in units of 2^(e - 127), E = e << 23, e 0 to 254
+  int lim = -1;                     // the largest scale of V that weights may take without a look; -1: no block yet, so that
+                                    // every unit's first block moves E and n
   bool fresh = true;
   for (; todo > 0; --todo) {
     if (fresh) {
@@ -322,6 +328,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
           const float x = __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
           qs[nt][c] = x < 0.f ? x : fmaxf(x, 1.4e-45f);
           n[nt][c] = kStart;
+          E[nt][c] = 0;
           odd = odd || !(qs[nt][c] >= 0.f && qs[nt][c] <= 1.f);
           l[nt][c] = 0.f;
         }
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][k][e] = 0.f;
       }
-      E = -1;
+      lim = -1;
     }
     cp_async_wait<kStages - 2>();
     __syncwarp();
@@ -388,43 +395,41 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
             for (int nt = 0; nt < NT; ++nt) sc[s][nt][2 * h] = sc[s][nt][2 * h + 1] = kNone;
     }
     // ---- weights
-    float w[G][NT][4], sum[NT][2];
+    float w[G][NT][4], sum[NT][2];  // (then in units of 2^E)
     bool slow = careful;
-    auto weigh = [&](int nt, int c) {
-      sum[nt][c] = 0.f;
-#pragma unroll
-      for (int s = 0; s < G; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[s][nt][2 * h + c] = ex2_approx(fmaf(sc[s][nt][2 * h + c], ks[s][h] * qs[nt][c], n[nt][c]));
-          sum[nt][c] += w[s][nt][2 * h + c];
-        }
-    };
 #pragma unroll
     for (int s = 0; s < G; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) slow = slow || vs[s][h] > E;
+      for (int h = 0; h < 2; ++h) slow = slow || vs[s][h] > lim;
+    int most = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        weigh(nt, c);
+        sum[nt][c] = 0.f;
+#pragma unroll
+        for (int s = 0; s < G; ++s) {
+          int x[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float p = ex2_approx(fmaf(sc[s][nt][2 * h + c], ks[s][h] * qs[nt][c], n[nt][c]));
+            sum[nt][c] += p;
+            // (within range: p is below 2^41 or its sum too large, V's scale at most kApart above E)
+            x[h] = __viaddmax_s32(__float_as_int(p), vs[s][h] - E[nt][c], 0);
+            w[s][nt][2 * h + c] = __int_as_float(x[h]);
+          }
+          most = __vimax3_s32(most, x[0], x[1]);
+        }
         slow = slow || !(sum[nt][c] <= kMost);         // (or NaN)
       }
-    if (__any_sync(0xffffffffu, slow)) {
-      // the maximum or V's largest scale moves (or the unit has a block of NaN)
-      int e1 = E;
+    if (__any_sync(0xffffffffu, slow || most > kTop)) {
+      // a maximum or E moves, or has to be looked at (or the unit has a block of NaN)
       bool bad = false;
 #pragma unroll
       for (int s = 0; s < G; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (vs[s][h] != kNaN) e1 = max(e1, vs[s][h]);
-          bad = bad || vs[s][h] == kNaN;
-        }
-      e1 = __reduce_max_sync(0xffffffffu, e1);
-      const float ae = pow2_neg((e1 - E) >> 23), spoil = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
-      E = e1;
+        for (int h = 0; h < 2; ++h) bad = bad || vs[s][h] == kNaN;
+      const float spoil = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fffffff) : 0.f;
       // the scores, one rounding each
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -446,6 +451,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
             }
         }
       bool rare = odd;
+      lim = 254 << 23;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float a[2];
@@ -458,22 +464,38 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
             for (int h = 0; h < 2; ++h) mx = fmaxf(mx, sc[s][nt][2 * h + c]);
 #pragma unroll
           for (int x = 4; x <= 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-          a[c] = 1.f;
+          int down = 0;             // how far the maximum moves
           if (mx + n[nt][c] > kUp + 6.f) {       // (not NaN: +inf on -inf)
             const float to = ceilf(kUp - mx);
-            a[c] = ex2_approx(to - n[nt][c]);
+            down = static_cast<int>(fminf(n[nt][c] - to, 512.f));
             n[nt][c] = to;
           }
           sum[nt][c] = 0.f;
+          uint32_t high = 0;        // the largest weight times its scale, exponents added
 #pragma unroll
           for (int s = 0; s < G; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              w[s][nt][2 * h + c] = ex2_approx(__fadd_rn(sc[s][nt][2 * h + c], n[nt][c]));
-              sum[nt][c] += w[s][nt][2 * h + c];
+              const float p = ex2_approx(__fadd_rn(sc[s][nt][2 * h + c], n[nt][c]));
+              sum[nt][c] += p;
+              w[s][nt][2 * h + c] = p;
+              if (p != 0.f) high = max(high, __float_as_uint(p) + static_cast<uint32_t>(vs[s][h]));
             }
-          l[nt][c] = fmaf(l[nt][c], a[c], spoil);
-          a[c] *= ae;
+#pragma unroll
+          for (int x = 4; x <= 16; x <<= 1) high = max(high, __shfl_xor_sync(0xffffffffu, high, x));
+          l[nt][c] = fmaf(l[nt][c], pow2_neg(down), spoil);
+          // the outputs' unit, by the move of the weights' or by this block: its largest is 2^7 to 2^8
+          const int was = (E[nt][c] >> 23) - down, e = min(max(max(was, static_cast<int>(high >> 23) - 134), 0), 254);
+          a[c] = pow2_neg(e - was);
+          E[nt][c] = e << 23;
+          lim = min(lim, min(E[nt][c], 190 << 23) + kApart);
+#pragma unroll
+          for (int s = 0; s < G; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int x = __viaddmax_s32(__float_as_int(w[s][nt][2 * h + c]), vs[s][h] - E[nt][c], 0);
+              if (w[s][nt][2 * h + c] != 0.f) w[s][nt][2 * h + c] = __int_as_float(x);
+            }
           rare = rare || !(fabsf(n[nt][c]) < kFar);
         }
 #pragma unroll
@@ -493,7 +515,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
           }
       }
     }
-    // ---- and their transposes as operands, in units of V's largest scale
+    // ---- and their transposes as operands
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -502,17 +524,15 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
 #pragma unroll
     for (int s = 0; s < G; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float f = __int_as_float(max(static_cast<int>(static_cast<unsigned>(vs[s][h]) - E + (127u << 23)), 0));
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float x = w[s][nt][2 * h] * f, y = w[s][nt][2 * h + 1] * f;
+          const float x = w[s][nt][2 * h], y = w[s][nt][2 * h + 1];
           const __half2 hi = __floats2half2_rn(x, y);
           ph[s][nt][h] = transpose8(*reinterpret_cast<const uint32_t*>(&hi));
           const float2 b = __half22float2(hi);
           pl[s][nt][h] = transpose8(half2_bits(x - b.x, y - b.y));
         }
-      }
     // ---- output
 #pragma unroll
     for (int s = 0; s < G; ++s) {
@@ -564,7 +584,6 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
       const int have = min(kRows, p.group - part * kRows);
       const bool all = whole && last;
       const long long piece = 2 * w_id + (later ? 1 : 0);   // as in the 16-bit kernel
-      const float unit = scale_of(E >> 23);
       const long long out0 = (static_cast<long long>(cc.i) * p.nh + head * p.group + part * kRows) * D;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -576,19 +595,17 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
           const int r = 8 * nt + 2 * t + c;
           if (r >= have) continue;
           float y[2 * KS];          // columns 2 KS g ..
-          const float inv = 1.f / sum;
+          // of a piece: by a power of two, so that the sum is 1 to 2 and no output above twice the largest value
+          const int up = sum > 0.f && sum < -kNone && fabsf(n[nt][c]) < 0x1p22f ? (__float_as_int(sum) >> 23) - 127 : 0;
+          const float by = all ? 1.f / sum : __int_as_float((127 - up) << 23), unit = scale_of(E[nt][c] >> 23);
 #pragma unroll
-          for (int e = 0; e < 2 * KS; ++e) {
-            y[e] = o[nt][e >> 1][2 * (e & 1) + c];
-            if (all) y[e] *= inv;
-            y[e] *= unit;
-          }
+          for (int e = 0; e < 2 * KS; ++e) y[e] = o[nt][e >> 1][2 * (e & 1) + c] * by * unit;
           if (all) {
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out0 + r * D + 2 * KS * g);
 #pragma unroll
             for (int e = 0; e < KS / 4; ++e) out[e] = p.bf16 ? pack16<__nv_bfloat16>(y + 8 * e) : pack16<__half>(y + 8 * e);
           } else {
-            if (g == 0) p.ml[piece * kRows + r] = make_float2(-n[nt][c], sum);
+            if (g == 0) p.ml[piece * kRows + r] = make_float2(static_cast<float>(up) - n[nt][c], sum * by);
             float4* acc = reinterpret_cast<float4*>(p.acc + (piece * rows_kept + r) * D + 2 * KS * g);
 #pragma unroll
             for (int e = 0; e < KS / 2; ++e) acc[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);

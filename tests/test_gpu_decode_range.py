@@ -203,3 +203,73 @@ def test_a_large_scale_and_large_queries_beside_tiny_keys(kind, lens):
         got = rpp.attention_decode(c, 0, q, scale=1e38)
         assert rpp.get_device_error(c.err) == 0
         close(got, want, EPS["bf16"], rest)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,nh,nkv", [(64, 4, 2), (128, 8, 2), (128, 20, 1)])
+@pytest.mark.parametrize("lens", [[2, 16, 40, 17, 33] * 60, [3000, 2, 700]], ids=["whole", "cut"])
+@pytest.mark.parametrize("order", ["near first", "far first", "in turn"])
+def test_values_far_apart(kind, dtype, d, nh, nkv, lens, order):
+    """Half of a sequence's blocks hold values up to 2^120 larger than the other half's, which the queries hardly look at, or
+    some heads at the ones and some at the others.  Error, beside the output's rounding (P_j: weights that add up to 1):
+    scores, exp2, P's parts and sums as in the other tests, of sum P_j |V_j|; half a step of f16's smallest for each key's
+    code, where the largest P_j 2^(b_j - 127) is held as 2^7 at least."""
+    if order == "in turn":
+        half = lambda n: (torch.arange(n, device=dev()) // 4) % 2 == 1
+    else:
+        half = lambda n: (torch.arange(n, device=dev()) >= (n + 1) // 2) ^ (order == "far first")
+    per = nh // nkv
+    for gap, away, mixed in ((20, 40.0, True), (20, 300.0, True), (45, 40.0, False), (45, 300.0, False), (45, 300.0, True),
+                             (100, 40.0, True), (100, 300.0, True), (120, 300.0, False)):
+        if dtype == "fp16" and (gap == 100 or gap == 45 and mixed):
+            continue                               # (beyond fp16's values)
+        c = t8.make(kind, lens, nkv, d, 16, 1, seed=gap, spread=1)
+        low = 127 - (12 if kind == "int8" else 14) if dtype == "fp16" else 60
+        for s, n in enumerate(lens):
+            page, row = places(c, s)
+            far = half(n)
+            k = torch.zeros((n, nkv, d), device=dev())
+            k[:, :, 0] = torch.where(far, -64.0, 64.0)[:, None]
+            k[:, :, 1] = torch.arange(n, device=dev())[:, None] % 64 - 32.0
+            c.pool.view(torch.uint8)[0, page, 0, :, row] = k.to(t8.CODES[kind]).view(torch.uint8)
+            c.scales[0, page, 0, :, row] = 121
+            c.scales[0, page, 1, :, row] = (low + gap * far.int())[:, None].to(torch.uint8)
+        q = torch.zeros((len(lens), nkv, per, d), device=dev())
+        q[..., 0] = away / 2 * d ** 0.5
+        if mixed:
+            q[:, :, 1::2, 0] *= -1
+        q[..., 1] = 1.5
+        q = q.to(TDT[dtype]).flatten(1)
+        got = rpp.attention_decode(c, 0, q)
+        assert rpp.get_device_error(c.err) == 0 and torch.isfinite(got.float()).all()
+        e = EPS[dtype]
+        for s in list(range(min(len(lens), 10))) + [len(lens) - 1]:
+            n = lens[s]
+            K, V, _ = t8.sequence(c, 0, s)
+            qi = q[s].double().view(nkv, per, d)
+            z = torch.einsum("hgd,nhd->hgn", qi, K) * d ** -0.5
+            P = torch.softmax(z, -1)
+            ref = torch.einsum("hgn,nhd->hgd", P, V)
+            page, row = places(c, s)
+            unit = torch.exp2(c.scales[0, page, 1, :, row].double() - 127).T[:, None]                # [nkv, 1, n]
+            codes = (V / unit[:, 0].T[..., None]).abs().sum(0)[:, None]                                # [nkv, 1, d]
+            mag = (torch.einsum("hgd,nhd->hgn", qi.abs(), K.abs()) * d ** -0.5).amax(-1)
+            ds = (d + 6) * 2.0 ** -24 * mag + 2.0 ** -22 * z.abs().amax(-1)
+            part = torch.einsum("hgn,nhd->hgd", P, V.abs())
+            limit = e / 2 * ref.abs() + (2 * ds + 2 * (2.0 ** -22 + 2.0 ** -21 + n * 2.0 ** -24))[..., None] * part + \
+                2.0 ** -32 * (P * unit).amax(-1, keepdim=True) * codes + (2.0 ** -25 if dtype == "fp16" else 2.0 ** -134)
+            off = (got[s].double().view(nkv, per, d) - ref).abs()
+            assert (off <= limit).all(), (gap, away, mixed, s, n, float((off / limit).max()))
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,nh,nkv", HEADS)
+@pytest.mark.parametrize("size", [110, 87, -60])
+def test_values_of_any_size_in_pieces(kind, d, nh, nkv, size):
+    """Units that several warps share: what they leave for the join is held in units of its own sum."""
+    lens = [3000, 1, 900, 20]
+    c = t8.make(kind, lens, nkv, d, 16, 16, spread=0)
+    c.scales[:, :, 1] = torch.where(c.scales[:, :, 1] == 255, 255, c.scales[:, :, 1].int() + size).to(torch.uint8)
+    q = t8.queries(len(lens), nh, d, "bf16", scale=3.0)
+    t8.check(rpp.attention_decode(c, 0, q), q, c, 0, range(len(lens)), nh)
