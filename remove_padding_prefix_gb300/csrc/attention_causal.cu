@@ -158,15 +158,15 @@ struct Walk {
     }
     it.b = s.perm[sq];
     it.h = idx - sq * s.nh;
-    it.c0 = __ldg(s.cu + it.b);
-    it.len = __ldg(s.cu + it.b + 1) - it.c0;
+    it.c0 = s.cu[it.b];
+    it.len = s.cu[it.b + 1] - it.c0;
     return it;
   }
 };
 
 // Builds the list (all threads) at `base`, with classes + 1 words at `cursor` for the time of the call.
 // False: the CTA must quit (error word set, or bad bounds, which are recorded).
-__device__ __forceinline__ bool build_list(const int32_t* __restrict__ cu, int B, int T_max, int max_len, int nh,
+__device__ __forceinline__ bool build_list(const int32_t* cu, int B, int T_max, int max_len, int nh,
                                            int classes, int32_t* err, int* s_status, uint8_t* base, int* cursor,
                                            List& out) {
   int16_t* perm = reinterpret_cast<int16_t*>(base);
@@ -178,7 +178,7 @@ __device__ __forceinline__ bool build_list(const int32_t* __restrict__ cu, int B
   if (*s_status) return false;
   __syncthreads();
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+    const int c0 = cu[b], c1 = cu[b + 1];
     const long long len = static_cast<long long>(c1) - c0;
     if (c0 < 0 || len < 0 || c1 > T_max || len > max_len) {
       atomicCAS(s_status, 0, len > max_len ? RPP_DERR_LENGTH : RPP_DERR_ROWS);
@@ -208,7 +208,7 @@ __device__ __forceinline__ bool build_list(const int32_t* __restrict__ cu, int B
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int b = b0 + lane;
       int c = 0;
-      if (b < B) c = (__ldg(cu + b + 1) - __ldg(cu + b) + kT - 1) / kT;
+      if (b < B) c = (cu[b + 1] - cu[b] + kT - 1) / kT;
       const unsigned peers = __match_any_sync(0xffffffffu, c);
       const int rank = __popc(peers & ((1u << lane) - 1u));
       if (c > 0) perm[cursor[c] + rank] = static_cast<int16_t>(b);
@@ -310,7 +310,7 @@ template <typename T, int D, bool PAIR>
 __global__ void __launch_bounds__((Shape<D, PAIR>::kThreads), (PAIR ? 1 : 2))
     attention_causal_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, int q_x, int k_x, int v_x,
-                            const T* __restrict__ k_rows, const T* __restrict__ v_rows, int kv_stride, const int32_t* __restrict__ cu, int B,
+                            const T* k_rows, const T* v_rows, int kv_stride, const int32_t* cu, int B,
                             int T_max, int max_len, int nh, int group, int classes, T* __restrict__ out,
                             float scale_log2, int32_t* err) {
   using S = Shape<D, PAIR>;

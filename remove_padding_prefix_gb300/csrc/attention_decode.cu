@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
 #pragma unroll
     for (int s = 0; s < KB / 16; ++s) {
       const int key = c.blk * KB + 16 * s;
-      page[s] = key < c.len ? __ldg(c.row + key / ps) : 0;
+      page[s] = key < c.len ? c.row[key / ps] : 0;
     }
   };
   auto issue = [&](const Cursor& c, int stage) {
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = g + (e & 1) * 8, c = 16 * k + 2 * t + (e >> 1) * 8;
-          qf[k][e] = r < have ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D + c)) : 0u;
+          qf[k][e] = r < have ? *reinterpret_cast<const uint32_t*>(q + r * D + c) : 0u;
         }
       }
 #pragma unroll
@@ -354,11 +354,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_decode_kernel(const 
         const int k1 = min(cc.len, (cc.blk + 1) * KB);
         float sum[E] = {};
         uint32_t got = 0;           // columns that have one
-        int next = __ldg(cc.row + (cc.blk + 1 - here) * KB / ps);
+        int next = cc.row[(cc.blk + 1 - here) * KB / ps];
 #pragma unroll 1
         for (int key = (cc.blk + 1 - here) * KB; key < k1; key += 8) {
           const int pg = next;      // read while the rows before were under way
-          if (key + 8 < k1) next = __ldg(cc.row + (key + 8) / ps);
+          if (key + 8 < k1) next = cc.row[(key + 8) / ps];
           if (pg < 0 || pg >= p.d.pages) continue;
           const T* kr = pool + pg * page_elems + head * head_elems + static_cast<long long>(key % ps) * D + lane * E;
           const T* vr = kr + v_off;

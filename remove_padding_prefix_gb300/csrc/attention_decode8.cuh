@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
   auto read_pages = [&]() {
 #pragma unroll
     for (int s = 0; s < G; ++s) {
-      page[s] = 16 * s < ld.left ? __ldg(table + at) : 0;    // past the sequence's end any page will do
+      page[s] = 16 * s < ld.left ? table[at] : 0;    // past the sequence's end any page will do
       rows[s] = row;
       row += 16;
       if (row == ps) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
         copy16(to + k_to + s * 1024 + i * 512, k + i * RG * D);
         copy16(to + (D == 128 && (i & 1) ? v_to ^ 64 : v_to) + s * 1024 + i * 512, v + i * RG * D);
       }
-      sc[s] = __ldg(sp + static_cast<long long>(page[s]) * p.page_scales + ((rows[s] + (lane & 15)) >> p.shift));
+      sc[s] = sp[static_cast<long long>(page[s]) * p.page_scales + ((rows[s] + (lane & 15)) >> p.shift)];
     }
     sc_left = ld.left;
     sc_to = ring_sc + stage * kScaleBytes + lane * 4;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
         for (int x = 0; x < D / 64; ++x)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint4 v = r < have ? __ldg(reinterpret_cast<const uint4*>(q + r * D + 64 * x + 16 * t) + y)
+            const uint4 v = r < have ? reinterpret_cast<const uint4*>(q + r * D + 64 * x + 16 * t)[y]
                                      : make_uint4(0u, 0u, 0u, 0u);
             w[x * 8 + y * 4] = v.x;
             w[x * 8 + y * 4 + 1] = v.y;

@@ -470,6 +470,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int ab_fmt, int M, int N) {
 // (griddepcontrol.wait: the predecessor has completed and its writes are visible)
 // before touching anything the predecessor produced, and lets its own successor
 // launch early.  Without the launch attribute both instructions are no-ops.
+// What a predecessor may still be writing while the kernel is resident is read with plain loads: the read-only path
+// (__ldg, const T* __restrict__) is for data that nobody writes during the kernel's whole life.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -171,9 +171,9 @@ struct Job {
 // offsets [n + 1], the slot bitmap.
 template <typename T, bool kI8, int D, int P, bool kFine>
 __global__ void __launch_bounds__(kMoveThreads, kAppendCtas)
-    kv8_append_kernel(Codes c, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
-                      const int32_t* __restrict__ refs, const T* __restrict__ k, const T* __restrict__ v, int row_stride,
-                      const int32_t* __restrict__ slots, const int32_t* __restrict__ cu, int n, int rows_max, int tok,
+    kv8_append_kernel(Codes c, const int32_t* table, const int32_t* lens,
+                      const int32_t* refs, const T* k, const T* v, int row_stride,
+                      const int32_t* slots, const int32_t* cu, int n, int rows_max, int tok,
                       int span, int32_t* err) {
   constexpr int GL = D / 8;             // lanes of a head's row
   constexpr int LPR = P * GL;           // lanes of a row
@@ -422,8 +422,8 @@ enum { kPlain16 = 0, kInt8 = 1, kE4m3 = 2 };
 // Dynamic shared memory: the list's offsets [n + 1].
 template <typename TO, int kCode>
 __global__ void __launch_bounds__(kMoveThreads, kReadCtas)
-    kv_read_kernel(Codes c, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
-                   const int32_t* __restrict__ slots, const int32_t* __restrict__ starts, const int32_t* __restrict__ cu,
+    kv_read_kernel(Codes c, const int32_t* table, const int32_t* lens,
+                   const int32_t* slots, const int32_t* starts, const int32_t* cu,
                    int n, int rows_max, int tok, int vshift, TO* __restrict__ k, TO* __restrict__ v, int row_stride,
                    int32_t* err) {
   using Vec8 = typename std::conditional<kCode == kPlain16, uint4, uint2>::type;     // eight values in the pool

@@ -47,7 +47,7 @@ __device__ __forceinline__ int warp_scan_incl(int v) {
 }
 
 // the four reference counts from page p on; pages past `pages` read as -1 (neither free nor live)
-__device__ __forceinline__ int4 load_refs4(const int32_t* __restrict__ refs, int p, int pages) {
+__device__ __forceinline__ int4 load_refs4(const int32_t* refs, int p, int pages) {
   if (p + 4 <= pages) return *reinterpret_cast<const int4*>(refs + p);
   int4 v = make_int4(-1, -1, -1, -1);
   if (p < pages) v.x = refs[p];
@@ -79,8 +79,8 @@ constexpr int kMostShares = 8192;     // kMostShares * kForkShare + 1 is an int
 static_assert(kForkShare > kKvMaxSlots && static_cast<long long>(kMostShares) * kForkShare < 0x7fffffffLL, "");
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads)
-    kv_reserve_kernel(KvDims d, int32_t* __restrict__ table, int32_t* __restrict__ lens, int32_t* __restrict__ refs,
-                      const int32_t* __restrict__ slots, const int32_t* __restrict__ counts_or_from, int n, int shares,
+    kv_reserve_kernel(KvDims d, int32_t* table, int32_t* lens, int32_t* refs,
+                      const int32_t* slots, const int32_t* counts_or_from, int n, int shares,
                       int32_t* err) {
   extern __shared__ int32_t s_need[];
   uint32_t* seen = reinterpret_cast<uint32_t*>(s_need + n + 1);
@@ -219,9 +219,9 @@ struct PageScales {
 // and a call that the plan refused finds no marks, whatever its lists and the state hold.
 template <bool kScales>
 __global__ void __launch_bounds__(kMoveThreads)
-    kv_fork_copy_kernel(KvDims d, PageScales q, uint4* __restrict__ pool, int32_t* __restrict__ table,
-                        const int32_t* __restrict__ lens, int32_t* __restrict__ refs, const int32_t* __restrict__ from,
-                        const int32_t* __restrict__ to, int n, int32_t* err) {
+    kv_fork_copy_kernel(KvDims d, PageScales q, uint4* __restrict__ pool, int32_t* table,
+                        const int32_t* lens, int32_t* refs, const int32_t* from,
+                        const int32_t* to, int n, int32_t* err) {
   pdl_wait();
   pdl_trigger();
   const int vpr = d.head_dim / 8;                                   // 16-byte vectors of a row
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 // A CTA takes slots blockIdx.x, + gridDim.x, ...; each CTA checks the whole list first, so
 // a slot out of range or given twice stops all of them before anything is changed.
 __global__ void __launch_bounds__(kMoveThreads)
-    kv_free_kernel(KvDims d, int32_t* __restrict__ table, int32_t* __restrict__ lens, int32_t* __restrict__ refs,
-                   const int32_t* __restrict__ slots, int n, int32_t* err) {
+    kv_free_kernel(KvDims d, int32_t* table, int32_t* lens, int32_t* refs,
+                   const int32_t* slots, int n, int32_t* err) {
   extern __shared__ uint32_t s_seen[];
   __shared__ Gate gate;
   pdl_wait();
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(kMoveThreads)
 // 16-byte copy.
 constexpr int kMaxTok = 32;
 __global__ void __launch_bounds__(kMoveThreads)
-    kv_append_kernel(KvDims d, uint4* __restrict__ pool_layer, const int32_t* __restrict__ table,
-                     const int32_t* __restrict__ lens, const int32_t* __restrict__ refs, const uint4* __restrict__ k,
-                     const uint4* __restrict__ v, int row_vec, const int32_t* __restrict__ slots,
-                     const int32_t* __restrict__ cu, int n, int rows_max, int tok, int32_t* err) {
+    kv_append_kernel(KvDims d, uint4* __restrict__ pool_layer, const int32_t* table,
+                     const int32_t* lens, const int32_t* refs, const uint4* k,
+                     const uint4* v, int row_vec, const int32_t* slots,
+                     const int32_t* cu, int n, int rows_max, int tok, int32_t* err) {
   extern __shared__ uint32_t s_seen[];
   __shared__ Gate gate;
   __shared__ long long s_at[kMaxTok];   // first vector of the row in the pool (head 0 of K), -1: none
@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 // page below it.  moves[0] = their number (-1: the error word was set), moves[1] = live, then (to, from)
 // pairs; remap[p] = the page's new number (-1: not in use).
 __global__ void __launch_bounds__(kPlanThreads)
-    kv_compact_plan_kernel(int pages, const int32_t* __restrict__ refs, int32_t* __restrict__ remap,
-                           int32_t* __restrict__ live_out, int32_t* __restrict__ moves, const int32_t* err) {
+    kv_compact_plan_kernel(int pages, const int32_t* refs, int32_t* remap,
+                           int32_t* live_out, int32_t* moves, const int32_t* err) {
   __shared__ int s_flag, s_live, s_low;
   __shared__ int s_warp[kPlanWarps];
   pdl_wait();
@@ -510,8 +510,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 template <bool kScales>
 __global__ void __launch_bounds__(kMoveThreads)
     kv_compact_move_kernel(KvDims d, PageScales q, uint4* __restrict__ pool, const int32_t* table,
-                           const int32_t* __restrict__ lens, const int32_t* refs, int32_t* table_out,
-                           int32_t* refs_out, const int32_t* __restrict__ remap, const int32_t* __restrict__ moves,
+                           const int32_t* lens, const int32_t* refs, int32_t* table_out,
+                           int32_t* refs_out, const int32_t* remap, const int32_t* moves,
                            int32_t* err) {
   pdl_wait();
   pdl_trigger();

@@ -23,8 +23,8 @@ __device__ __forceinline__ bool len_ok(int len, const KvDims& d) {
 struct Gate {
   int quit, bad, back;
 };
-__device__ __forceinline__ bool pass(const int32_t* __restrict__ slots, int n, int first, const KvDims& d,
-                                     uint32_t* seen, Gate* g, int32_t* err, const int32_t* __restrict__ cu = nullptr,
+__device__ __forceinline__ bool pass(const int32_t* slots, int n, int first, const KvDims& d,
+                                     uint32_t* seen, Gate* g, int32_t* err, const int32_t* cu = nullptr,
                                      int c0 = 0, int c1 = 0) {
   if (threadIdx.x == 0) {
     g->quit = device_error_set(err) ? 1 : 0;
