@@ -18,8 +18,8 @@ constexpr int kD = 64;   // head dim
 
 // fp32 attention for fp32 layers: one thread per query row, keys staged through smem
 constexpr int kF32Rows = 64;
-__global__ void __launch_bounds__(kF32Rows) attention_varlen_f32_kernel(const float* __restrict__ qkv,
-                                                                        const int32_t* __restrict__ cu, int T_max,
+__global__ void __launch_bounds__(kF32Rows) attention_varlen_f32_kernel(const float* qkv,
+                                                                        const int32_t* cu, int T_max,
                                                                         int max_len, int nh,
                                                                         float* __restrict__ out, float scale,
                                                                         int32_t* err) {

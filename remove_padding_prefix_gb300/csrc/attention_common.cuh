@@ -91,7 +91,7 @@ __device__ __forceinline__ Item decode(const Sched& s, int g) {
 // Builds the item list in shared memory (`sched` points at sched_bytes(B) bytes).  Called
 // by every thread of the CTA (it holds __syncthreads).  Returns false when the CTA must
 // quit: an error word already set, or bad sequence bounds (recorded in err).
-__device__ __forceinline__ bool build_items(const int32_t* __restrict__ cu, int B, int T_max, int max_len, int nh,
+__device__ __forceinline__ bool build_items(const int32_t* cu, int B, int T_max, int max_len, int nh,
                                             int n_cls, int32_t* err, int* s_status, uint8_t* sched, Sched& out) {
   int* cls_cnt = reinterpret_cast<int*>(sched);
   int* seq_off = cls_cnt + (kMaxCls + 2);
@@ -104,7 +104,7 @@ __device__ __forceinline__ bool build_items(const int32_t* __restrict__ cu, int 
   for (int c = threadIdx.x; c < kMaxCls + 2; c += nthreads) cls_cnt[c] = 0;
   __syncthreads();
   if (*s_status) return false;
-  for (int b = threadIdx.x; b <= B; b += nthreads) s_cu[b] = __ldg(cu + b);
+  for (int b = threadIdx.x; b <= B; b += nthreads) s_cu[b] = cu[b];
   __syncthreads();
   for (int b = threadIdx.x; b < B; b += nthreads) {
     const int c0 = s_cu[b], c1 = s_cu[b + 1], len = c1 - c0;

@@ -73,7 +73,7 @@ size_t smem_bytes(int B) { return 1024 + kOffSched + sched_bytes(B); }
 // device memory (the input quantisation of the output projection, fused).
 template <typename T, bool I8, bool QO>
 __global__ void __launch_bounds__(kThreads, 2)
-attention_sched_kernel(const __grid_constant__ CUtensorMap tm, const int32_t* __restrict__ cu, int B, int T_max,
+attention_sched_kernel(const __grid_constant__ CUtensorMap tm, const int32_t* cu, int B, int T_max,
                        int max_len, int nh, int n_cls, void* __restrict__ out_v, float scale_log2,
                        const float* __restrict__ i8_scales, const float* __restrict__ out_scale, int32_t* err) {
   using TOut = typename std::conditional<QO, __nv_bfloat16, typename std::conditional<I8, __half, T>::type>::type;

@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 
 template <typename T>
 __global__ void __launch_bounds__(kAttnThreads, 2) attention_tc_kernel(const __grid_constant__ CUtensorMap tm,
-                                                                    const int32_t* __restrict__ cu, int T_max,
+                                                                    const int32_t* cu, int T_max,
                                                                     int max_len, int nh, T* __restrict__ out,
                                                                     float scale_log2, int32_t* err) {
   pdl_wait();

@@ -14,7 +14,7 @@ constexpr int kT = 64;
 constexpr int kK = 16;
 
 template <int EPI>
-__global__ void __launch_bounds__(256) gemm_f32_kernel(const float* __restrict__ A, const float* __restrict__ W,
+__global__ void __launch_bounds__(256) gemm_f32_kernel(const float* A, const float* __restrict__ W,
                                                        const float* __restrict__ bias, const float* residual,
                                                        float* out, int M_max, const int32_t* rows, int N, int K,
                                                        int32_t* err) {

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(128) layernorm_kernel(LnArgs a) {
 
 // per-tensor symmetric int8 quantisation of [M, H] (8 elements per thread step)
 template <typename T>
-__global__ void quantize_kernel(const T* __restrict__ x, const float* scale, int8_t* __restrict__ q, int M_max,
+__global__ void quantize_kernel(const T* x, const float* scale, int8_t* __restrict__ q, int M_max,
                                 const int32_t* rows, int H, int32_t* err) {
   pdl_wait();
   pdl_trigger();
@@ -358,7 +358,7 @@ __global__ void quantize_kernel(const T* __restrict__ x, const float* scale, int
 
 // max |x| over [M, H] (8 elements per thread step), accumulated into *amax
 template <typename T>
-__global__ void amax_kernel(const T* __restrict__ x, int M_max, const int32_t* rows, int H, float* amax,
+__global__ void amax_kernel(const T* x, int M_max, const int32_t* rows, int H, float* amax,
                             int32_t* err) {
   pdl_wait();
   pdl_trigger();
@@ -590,7 +590,7 @@ bool ln_stream_applies(const LnArgs& a) {
 // max |x| of each part of [M, W] rows cut into column parts of width part_w (at most
 // three: the Q, K and V parts of the QKV projection), accumulated into amax[part]
 template <typename T>
-__global__ void amax_parts_kernel(const T* __restrict__ x, int M_max, const int32_t* rows, int W, int part_w,
+__global__ void amax_parts_kernel(const T* x, int M_max, const int32_t* rows, int W, int part_w,
                                   float* amax, int32_t* err) {
   pdl_wait();
   pdl_trigger();

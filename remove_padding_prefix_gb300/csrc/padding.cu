@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 
-__global__ void __launch_bounds__(kScanThreads) build_offsets_kernel(const int32_t* __restrict__ lengths, int B,
+__global__ void __launch_bounds__(kScanThreads) build_offsets_kernel(const int32_t* lengths, int B,
                                                                      int L, int32_t* __restrict__ cu,
                                                                      int32_t* __restrict__ padding_offset,
                                                                      int32_t* err) {
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kScanThreads) build_offsets_kernel(const int32
 }
 
 // packed[i] = padded[i + po[i]] for i < T; VPR 16-byte vectors per row
-__global__ void remove_padding_kernel(const uint4* __restrict__ padded, const int32_t* __restrict__ po,
-                                      const int32_t* __restrict__ cu, int B, int T_max, int vpr,
+__global__ void remove_padding_kernel(const uint4* padded, const int32_t* po,
+                                      const int32_t* cu, int B, int T_max, int vpr,
                                       uint4* __restrict__ packed, int32_t* err) {
   pdl_wait();
   pdl_trigger();
@@ -96,12 +96,12 @@ __global__ void remove_padding_kernel(const uint4* __restrict__ padded, const in
       set_device_error(err, RPP_DERR_ROWS);
       continue;
     }
-    packed[v] = __ldg(padded + static_cast<long long>(src_row) * vpr + c);
+    packed[v] = padded[static_cast<long long>(src_row) * vpr + c];
   }
 }
 
 // padded[b*L + p] = p < len_b ? packed[cu[b] + p] : 0
-__global__ void rebuild_padding_kernel(const uint4* __restrict__ packed, const int32_t* __restrict__ cu, int B,
+__global__ void rebuild_padding_kernel(const uint4* packed, const int32_t* cu, int B,
                                        int L, int vpr, uint4* __restrict__ padded, int32_t* err) {
   pdl_wait();
   pdl_trigger();
@@ -116,7 +116,7 @@ __global__ void rebuild_padding_kernel(const uint4* __restrict__ packed, const i
     const int32_t c0 = cu[b];
     const int32_t len = cu[b + 1] - c0;
     uint4 val = make_uint4(0u, 0u, 0u, 0u);
-    if (p < len) val = __ldg(packed + (static_cast<long long>(c0) + p) * vpr + c);
+    if (p < len) val = packed[(static_cast<long long>(c0) + p) * vpr + c];
     padded[v] = val;
   }
 }
@@ -128,8 +128,8 @@ __global__ void rebuild_padding_kernel(const uint4* __restrict__ packed, const i
 constexpr int kFusedMaxB = 1024;
 constexpr int kFusedThreads = 256;
 
-__global__ void __launch_bounds__(kFusedThreads) offsets_remove_kernel(const int32_t* __restrict__ lengths, int B,
-                                                                       int L, int vpr, const uint4* __restrict__ padded,
+__global__ void __launch_bounds__(kFusedThreads) offsets_remove_kernel(const int32_t* lengths, int B,
+                                                                       int L, int vpr, const uint4* padded,
                                                                        int32_t* __restrict__ cu,
                                                                        int32_t* __restrict__ po,
                                                                        uint4* __restrict__ packed, int32_t* err) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kFusedThreads) offsets_remove_kernel(const int
       uint4 t[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (c + 32 * u < vpr) t[u] = __ldg(src + c + 32 * u);
+        if (c + 32 * u < vpr) t[u] = src[c + 32 * u];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         if (c + 32 * u < vpr) dst[c + 32 * u] = t[u];

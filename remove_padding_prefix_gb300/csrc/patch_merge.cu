@@ -19,7 +19,7 @@ namespace rpp {
 namespace {
 
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) patch_merge_ln_kernel(const T* __restrict__ x, int B, int I, int C,
+__global__ void __launch_bounds__(256) patch_merge_ln_kernel(const T* x, int B, int I, int C,
                                                              const float* __restrict__ gamma,
                                                              const float* __restrict__ beta, float eps,
                                                              T* __restrict__ out, int32_t* err) {

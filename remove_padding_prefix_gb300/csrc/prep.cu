@@ -71,7 +71,7 @@ __global__ void weight_quant_kernel(const void* w, rpp_dtype dt, int K, int N, c
 }
 
 template <typename T>
-__global__ void codes_bf16_kernel(const T* __restrict__ x, const float* scale, __nv_bfloat16* __restrict__ codes,
+__global__ void codes_bf16_kernel(const T* x, const float* scale, __nv_bfloat16* __restrict__ codes,
                                   int M_max, const int32_t* rows, int H, int32_t* err) {
   pdl_wait();
   pdl_trigger();

@@ -70,7 +70,7 @@ template <typename T, int EW>
 __global__ void __launch_bounds__(mlp_threads<EW>(), 1)
 swin_mlp_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW1,
                 const __grid_constant__ CUtensorMap tmW2, const float* __restrict__ b1, const float* __restrict__ b2,
-                const T* __restrict__ resid, T* __restrict__ out, int M, int32_t* err) {
+                const T* resid, T* __restrict__ out, int M, int32_t* err) {
   constexpr int fmt = MlpFmt<T>::v;
   constexpr uint32_t IDESC_FC1 = idesc_f16(fmt, kMBM, 64) | (1u << 16);   // B (W1 panel) MN-major
   constexpr uint32_t IDESC_FC2 = idesc_f16(fmt, kMBM, kMC);

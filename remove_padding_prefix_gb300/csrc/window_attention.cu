@@ -79,7 +79,7 @@ __device__ __forceinline__ int region(int c, int I, int w, int s) { return c < I
 // one FMA and a select per element.  The next window's rows are gathered (cp.async)
 // into the second of two shared-memory buffers while the current one is computed.
 template <typename T>
-__global__ void __launch_bounds__(128, 4) window_attention_kernel(const T* __restrict__ qkv,
+__global__ void __launch_bounds__(128, 4) window_attention_kernel(const T* qkv,
                                                                   const float* __restrict__ bias,
                                                                   T* __restrict__ out, int I, int w, int s, int nh,
                                                                   long long n_win, float scale_log2, int32_t* err) {
