@@ -582,12 +582,14 @@ def kv_read(cache: KvCache, layer: int, slots, cu_seqlens=None, starts=None, row
     Rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 (row i without cu_seqlens) receive the tokens of slots[i] from position
     starts[i] on, or its last ones without starts.  k, v: where they go, [rows, kv_heads * head_dim]
     each (columns of one wider tensor will do; rows behind the last sequence stay as they are); without
-    them a new tensor of ``rows`` rows (needed with cu_seqlens) and ``dtype`` (of a KvCache8: fp16 or bf16, bf16
-    by default) is made."""
+    them a new tensor of ``rows`` rows (at least one; needed with cu_seqlens) and ``dtype`` (of a KvCache8: fp16 or bf16,
+    bf16 by default) is made."""
     err = cache.err if err is None else err
     n, w = slots.numel(), cache._width
     if (k is None) != (v is None):
         raise ValueError("k and v: expected both or neither")
+    if isinstance(dtype, str):
+        dtype = torch_dtype(dtype)
     if k is None:
         if rows is None:
             if cu_seqlens is not None:
@@ -595,14 +597,14 @@ def kv_read(cache: KvCache, layer: int, slots, cu_seqlens=None, starts=None, row
             rows = n
         if dtype is None:
             dtype = torch.bfloat16 if isinstance(cache, KvCache8) else cache._dtype
-        elif isinstance(dtype, str):
-            dtype = torch_dtype(dtype)
         got, code = cache._rows_dtype(dtype)
         if got is not dtype:
             raise ValueError(f"dtype: a cache of {got} has no rows of {dtype}")
         k, v = (_made(stream, torch.empty, (rows, w), dtype=dtype, device=cache.pool.device) for _ in range(2))
         ld = w
     else:
+        if (rows is not None and rows != k.shape[0]) or (dtype is not None and dtype is not k.dtype):
+            raise ValueError("rows and dtype: k and v, which are given, have their own")
         rows = k.shape[0]
         dtype, code = cache._rows_dtype(k.dtype)
         ld = _rows("k", k, w, dtype)
