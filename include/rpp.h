@@ -660,8 +660,8 @@ RPP_API rpp_status rpp_kv8_read(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cac
 /* As rpp_attention_decode, over the values code * 2^(b - 127); q and out of dtype, RPP_F16 or RPP_BF16.  Every head
  * that sees a block of NaN is NaN.  Scores are fp32: one beyond its largest is infinite, and weights under 2^-126 of the
  * largest are 0.  Weights p, times their value's scale, are rounded to two f16 parts for their product with the codes:
- * together off by up to 2^-22 of each, and 2^-32 of a head's largest p 2^(b - 127).  Sums are fp32 (values above 2^114 may
- * overflow them in sequences of thousands of tokens). */
+ * together off by up to 2^-22 of each, and 2^-32 of a head's largest p 2^(b - 127).  Sums are fp32 (values above 2^114,
+ * and 2^96 where scores pass 2^22, may overflow them in sequences of thousands of tokens). */
 RPP_API size_t rpp_attention_decode8_workspace_bytes(const rpp_kv8_cfg* cfg, int n, int nh);
 RPP_API rpp_status rpp_attention_decode8(const rpp_kv8_cfg* cfg, const rpp_kv8_cache* cache, int layer, const void* q,
                                          rpp_dtype dtype, int q_stride, const int32_t* slots, int n, int nh, float scale,

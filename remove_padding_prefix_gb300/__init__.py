@@ -512,7 +512,10 @@ class KvCache8(KvCache):
 
     @classmethod
     def from_tensors(cls, pool, scales, table, lens, refs):
-        """A cache over arrays that the caller holds already (kept, not copied)."""
+        """A cache over arrays that the caller holds already (kept, not copied).
+
+        scales: bytes 0 to 248, as rows of 16 bits give them, or 255 (NaN).  Those between stand for 2^122 to 2^127, but
+        the attention takes K's of 254 for infinite."""
         c = cls.__new__(cls)
         c.scales = scales
         c._bind(pool, table, lens, refs)

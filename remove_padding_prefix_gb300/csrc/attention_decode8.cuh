@@ -13,7 +13,7 @@
 //    key rows g and g + 8 (Q's fragments take the same order), of V the columns 16 g .. of four keys, paired across
 //    keys by byte permutations (the output's rows take that order).
 //  * A warp keeps its own ring of blocks (cp.async, 16 bytes a lane), chunks moved inside their 128-byte line so that no
-//    reading meets a bank twice: 64 to 147 KB an SM on their way or in use.  Reading the cache straight into operand
+//    reading meets a bank twice: 98 to 147 KB an SM on their way or in use.  Reading the cache straight into operand
 //    registers, without the ring, leaves too few bytes on their way: 128 sequences of 200 to 8192 keys, d = 128, 32 heads
 //    on 8, e4m3: 238 us, with the ring then 190 (182 now); with blocks brought to L2 ahead by bulk prefetches 275 and more.
 //  * Codes become f16 (exact for both types), so the products are exact in fp32.  fp16 queries are taken as they are; a bf16
@@ -33,7 +33,7 @@
 //    maximum first and rounds each product as it does there.  A score is infinite where it passes fp32's largest.
 //  * P^T comes out of the scores' registers by two 8 x 8 transposes (movmatrix).  P is split into two f16
 //    parts (p and what rounding p left), as in the 16-bit kernel; that costs nothing in the batch above, and cost 2 us of 61
-//    for 131000 keys of 16 heads, int8, d = 64 (50 now).
+//    for 131000 keys of 16 heads, int8, d = 64 (50.5 now).
 //
 // Codes past the sequence may be anything: their scores are -inf, their codes zeros.
 #pragma once
@@ -96,11 +96,11 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 }
 
 constexpr int kBlockBytes = 2048;                            // of K, and of V
-// Warps of a CTA (one an SM) and stages of a warp's ring.  Up to 8 query heads, d = 128: 12 and 3, 181 us for 128 sequences of
-// 200 to 8192 keys (e4m3); 16 and 3: 192, 16 and 2: 184, 12 and 4: 183, 12 and 2: 188.  d = 64 (twice the keys and
-// so the instructions for the same bytes): 16 and 2, 49.8 us for 131000 keys of 16 heads (int8); 12 and 3: 55.1, 14 and
-// 3: 55.0.  More than 8 heads: registers for 8 warps at d = 128 (3 stages 30.5 us, 6: 33 for 48 sequences of
-// 1000 to 6000 keys, 32 heads on 2; 12 warps that spill 33), 12 at d = 64 (192 sequences 56 us, with 8 warps 74).
+// Warps of a CTA (one an SM) and stages of a warp's ring.  Up to 8 query heads, d = 128: 12 and 3, 182 us for 128 sequences of
+// 200 to 8192 keys (e4m3); 16 and 2: 185 (but 2048 sequences of 20 keys 56.2 instead of 58.3), 12 and 2: 189.  d = 64 (twice
+// the keys and so the instructions for the same bytes): 16 and 2, 50.3 us for 131000 keys of 16 heads (int8); 12 and 3:
+// 55.4.  More than 8 heads: registers for 8 warps at d = 128 (3 stages 31.3 us, 4: 32.0, 2: 31.4 for 48 sequences of
+// 1000 to 6000 keys, 32 heads on 2), 12 and 3 at d = 64 (192 sequences 61 us, 2 stages 70, 8 warps 80).
 template <int D, int NT> struct Shape8 {
   static constexpr int kWarps = NT == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
   static constexpr int kStages = NT == 1 && D == 64 ? 2 : 3;
@@ -283,13 +283,12 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
     if (fresh) {
       const int head = head_of(cc.unit), part = cc.unit - head * p.parts;
       const int have = min(kRows, p.group - part * kRows);
-      fresh = false;
+      fresh = odd = false;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<long long>(cc.i) * p.q_stride +
                           static_cast<long long>(head * p.group + part * kRows) * D;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + g;
-        if (nt == 0) odd = false;
         uint32_t w[2 * KS];
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)

@@ -41,7 +41,7 @@ template <bool kI8>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   if constexpr (kI8) {
     // 1.5 * 2^23 added: the sum's last bits are the rounded integer
-    constexpr float kMagic = 12582912.f, kTop = 127.f;
+    constexpr float kMagic = 12582912.f, kTop = Code8<true>::kTop;
     const uint32_t x = __float_as_uint(fminf(fmaxf(a, -kTop), kTop) + kMagic);
     const uint32_t y = __float_as_uint(fminf(fmaxf(b, -kTop), kTop) + kMagic);
     const uint32_t z = __float_as_uint(fminf(fmaxf(c, -kTop), kTop) + kMagic);

@@ -5,7 +5,8 @@
 //   b = the smallest byte at which a is no more than half a step past the largest code,
 //       or the block's own where it has rows already and that is larger;
 //   code = x * 2^(127 - b), rounded half to even; codes the block has are rounded again where b grew.
-// Two bytes in and one out per value and no reuse: bound by HBM, with some 16 issue slots a value on the side.  The first
+// Two bytes in and one out per value and no reuse: HBM is the floor, latency the bound (7.5 instructions a value, 1.5 a cycle
+// of 4, DRAM at 41% for 24 prompts of 16181 rows: a head's rows are asked for when the head before is done).  The first
 // warp of a CTA finds where 16-row tiles (or blocks, if those are longer) and sequences begin among up to 32 packed
 // rows; then the warps share the tiles' heads: a warp looking on its own does that for every head again, a third of all
 // instructions with 8 heads (24 prompts, 16181 rows, d = 128: 26 us, this way 22.8).  A warp takes
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kMaxTok = 32;     // packed rows that a warp looks at together (a lane each)
-constexpr int kAppendCtas = 4;  // CTAs of an append that an SM holds (64 registers)
+constexpr int kAppendCtas = 4;  // CTAs of an append that an SM holds (64 registers, which spill 24 to 84 bytes but for P = 1, D = 64, kFine)
 constexpr int kReadCtas = 3;    // and of a read (80)
 
 // The packed row t of a call: its sequence, and how far from its end (1: the last token; below 1: nobody's row).
@@ -581,8 +582,10 @@ cudaError_t launch_kv8_append(const KvDims& d, const KvState& s, const Kv8Scales
 cudaError_t launch_kv_read(const KvDims& d, const KvState& s, const Kv8Scales* q, int layer, const int32_t* slots,
                            const int32_t* starts, const int32_t* cu, int n, int rows_max, void* k, void* v,
                            rpp_dtype dtype, int row_stride, int32_t* err, cudaStream_t stream) {
-  // One wave of warps, with equal shares of the rows.  16281 rows of 8 heads, d = 128: 20.8 us, in two waves 23.4; with a
-  // fourth CTA an SM (64 registers, four vectors fewer on their way) 59900 rows take 72 us instead of 66.
+  // Up to 32 rows a warp one wave of warps, with equal shares of the rows.  16281 rows of 8 heads, d = 128: 20.8 us, in two
+  // waves 23.4; with a fourth CTA an SM (64 registers, four vectors fewer on their way) 59900 rows take 72 us instead of 66.
+  // Above that (116000 rows) up to 8 CTAs an SM that come as others go, not one wave that strides: 300000 rows of 8 heads
+  // 302 us, one wave 316; 16 heads, d = 64, 312 and 336; 2 heads, d = 128, 112 and 110.
   const long long warps = static_cast<long long>(kReadCtas) * num_sms() * kMoveWarps;
   const long long passes = (rows_max + warps * kMaxTok - 1) / (warps * kMaxTok);
   const int tok = static_cast<int>((rows_max + warps * passes - 1) / (warps * passes));
