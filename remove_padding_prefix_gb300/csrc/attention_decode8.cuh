@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
   const int rows_kept = p.group < kRows ? p.group : kRows;
   uint32_t qf[NT][KS][2];
   float qs[NT][2];                  // scale (to base 2) of the scores of query heads 2t, 2t + 1, times 1/2; where that is infinite
-                                    // minus 2^-128 times it
+                                    // minus 2^-128 times it (-1 or less), where it is below 2^-126 minus 2^64 times it
   float o[NT][KS][4];               // heads 2t, 2t + 1 of an even column, then of the odd one after it
   float l[NT][2];                   // sums of the weights 2^(score + n):
   float n[NT][2];                   // kUp - maximum, a whole number; kStart before the first one, so that any score passes kMost
@@ -309,10 +309,11 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
           most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
           most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
           const int field = most >> 7;           // of the largest element; 255: no number, its head's output is NaN
-          const int up = field == 255 ? 0 : min(7 + 127 - field, 110);   // (at 110 every bf16 is exact)
+          const int up = field == 255 || most == 0 ? 0 : min(7 + 127 - field, 110);   // (at 110 every bf16 is exact)
           const float f_up = __int_as_float((127 + up) << 23);
           const float by = __int_as_float((127 - up) << 23);
-          back = back * by < __int_as_float(0x7f800000) ? back * by : -(back * 0x1p-64f * (by * 0x1p-64f));
+          const float x = back * by;
+          back = x == __int_as_float(0x7f800000) ? -(back * 0x1p-64f * (by * 0x1p-64f)) : x < 0x1p-126f ? -(back * 0x1p64f * by) : x;
 #pragma unroll
           for (int e = 0; e < 2 * KS; ++e)
             w[e] = half2_bits(__uint_as_float(w[e] << 16) * f_up, __uint_as_float(w[e] & 0xffff0000u) * f_up);
@@ -436,9 +437,10 @@ __global__ void __launch_bounds__(Shape8<D, NT>::kWarps * 32, 1) attention_decod
         for (int c = 0; c < 2; ++c) {
           float f = qs[nt][c], up = 1.f, more = 1.f;
           if (odd) {                // powers of two kept for last: 0 times what would be infinite is 0
-            if (f < 0.f) more = 0x1p64f;
-            if (f < 0.f || f > 1.f) up = 0x1p64f;
-            f = f < 0.f ? -f : f > 1.f ? f * 0x1p-64f : f;
+            if (f <= -1.f) more = 0x1p64f;
+            if (f <= -1.f || f > 1.f) up = 0x1p64f;
+            else if (f < 0.f) up = 0x1p-64f;
+            f = f > 1.f ? f * 0x1p-64f : fabsf(f);
           }
 #pragma unroll
           for (int s = 0; s < G; ++s)

@@ -203,6 +203,20 @@ def test_a_large_scale_and_large_queries_beside_tiny_keys(kind, lens):
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("lens", [WHOLE, CUT], ids=["whole", "cut"])
+@pytest.mark.parametrize("q_up", [-20, -41, -60, -90])
+def test_a_tiny_scale_and_tiny_queries_beside_large_keys(kind, lens, q_up):
+    """scale times the power of two that queries are held in is below fp32's smallest normal number (at 2^-144 a step is 2^-5
+    of it), the scores are about 2^-9."""
+    nkv, d, nh = 2, 64, 6
+    c = t8.make(kind, lens, nkv, d, 16, 16, spread=0)
+    c.scales[:, :, 0] = torch.where(c.scales[:, :, 0] != 255, 246, 255).to(torch.uint8)
+    q = t8.queries(len(lens), nh, d, "bf16", scale=2.0 ** q_up)
+    scale = 2.0 ** (-137 - q_up) * 1.37
+    t8.check(rpp.attention_decode(c, 0, q, scale=scale), q, c, 0, range(len(lens)), nh, scale=scale)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("d,nh,nkv", [(64, 4, 2), (128, 8, 2), (128, 20, 1)])
 @pytest.mark.parametrize("lens", [[2, 16, 40, 17, 33] * 60, [3000, 2, 700]], ids=["whole", "cut"])
